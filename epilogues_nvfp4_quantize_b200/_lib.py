@@ -27,12 +27,29 @@ EXPORTS = (
     "nvfp4_quantize_noalloc", "nvfp4_fake_quantize", "gemm_nvfp4_pointwise",
     "mxfp4_sf_bytes", "mxfp4_quantize", "gemm_mxfp4_pointwise", "gemm_mxfp4_plain",
     "gemm_mxfp4_rmsnorm", "gemm_mxfp4_swiglu", "gemm_nvfp4_reduce_rows_f32", "nvfp4_signal_barrier",
+    "gemv_nvfp4", "residual_norm", "residual_norm_backward", "residual_norm_workspace_bytes", "rope_axes",
 )
 
 
 class _Tensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("gscale", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+_i64, _vp, _i32, _f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+
+
+class _NormInputs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("batches", _i64), ("offsets", _vp), ("stream_dtype", _i32),
+                ("mod_dtype", _i32), ("norm", _i32), ("post_norm", _i32), ("residual_scale", _f32), ("eps", _f32),
+                ("x", _vp), ("ldx", _i64), ("y", _vp), ("ldy", _i64), ("gate", _vp), ("ldgate", _i64),
+                ("scale", _vp), ("ldscale", _i64), ("shift", _vp), ("ldshift", _i64), ("w_post", _vp), ("w", _vp)]
+
+
+class _NormGrads(ctypes.Structure):
+    _fields_ = [("dx_out", _vp), ("lddxo", _i64), ("dh", _vp), ("lddh", _i64), ("dx", _vp), ("lddx", _i64),
+                ("dy", _vp), ("lddy", _i64), ("dgate", _vp), ("lddgate", _i64), ("dscale", _vp), ("lddscale", _i64),
+                ("dshift", _vp), ("lddshift", _i64), ("dw", _vp), ("dw_post", _vp)]
 
 
 _lib = None
@@ -71,6 +88,12 @@ def load() -> ctypes.CDLL:
         "gemm_mxfp4_rmsnorm": (i32, [_Tensor, _Tensor, vp, i32, i64, f32, vp, i64, vp]),
         "gemm_mxfp4_swiglu": (i32, [_Tensor, _Tensor, vp, i64, ctypes.POINTER(_Tensor), vp]),
         "nvfp4_signal_barrier": (i32, [vp, i32, i32, ctypes.c_uint32, i64, vp]),
+        "gemv_nvfp4": (i32, [vp, i32, i64, i64, i32, _Tensor, vp, i32, vp, i64, vp]),
+        "residual_norm": (i32, [ctypes.POINTER(_NormInputs), vp, i64, vp, i64, ctypes.POINTER(_Tensor), vp, vp]),
+        "residual_norm_workspace_bytes": (i64, [i64, i64, i64]),
+        "residual_norm_backward": (i32, [ctypes.POINTER(_NormInputs), vp, ctypes.POINTER(_NormGrads), vp, vp]),
+        "rope_axes": (i32, [vp, i32, i64, i64, i64, i64, i64, vp, i32, i64, i32, ctypes.POINTER(ctypes.c_int32), vp,
+                            i32, i32, vp, i64, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -336,6 +359,313 @@ class FakeQuantizeSTE(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_y):
         return grad_y, None, None
+
+
+# ---- operators between the GEMMs of a layer -------------------------------------------
+def _same_device(*tensors: Optional[torch.Tensor]) -> torch.device:
+    """The one CUDA device that all given tensors are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _call(fn, what: str, dev: torch.device, stream, *args) -> None:
+    """Call `fn` with `dev` current (the library launches on the current device), on `stream` or
+    on that device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status:
+        _check(status, what)
+
+
+ACT_SILU = 2
+
+
+def gemv_nvfp4(x: torch.Tensor, B: NVFP4Tensor, D: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               silu: bool = False, stream=None) -> torch.Tensor:
+    """D = cast(f(x) (G B)^T + bias) for a few rows x (M x K, bf16 or f16) and an NVFP4 weight B
+    (N x K); f is the identity or SiLU; D (M x N) is bf16, f16 or f32 (see gemv_nvfp4 in the
+    header)."""
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16) or x.stride(1) != 1:
+        raise ValueError("x must be a 2-D bf16 or f16 tensor with unit column stride")
+    if D.dtype not in _OUT_KIND or D.dim() != 2 or D.stride(1) != 1:
+        raise ValueError("D must be a 2-D bf16, f16 or f32 tensor with unit column stride")
+    M, K = x.shape
+    if K != B.cols or D.shape[0] != M or D.shape[1] != B.rows:
+        raise ValueError(f"x is {M} x {K}, B {B.rows} x {B.cols} and D {tuple(D.shape)}")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (B.rows,) or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous float32 tensor with one value per row of B")
+    dev = _same_device(x, D, B.codes, B.sf, B.gscale, bias)
+    _call(load().gemv_nvfp4, "gemv_nvfp4", dev, stream, x.data_ptr(), _OUT_KIND[x.dtype], M, _ld(x),
+          ACT_SILU if silu else ACT_NONE, B.c(), _ptr(bias), _OUT_KIND[D.dtype], D.data_ptr(), _ld(D))
+    return D
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row pitch of a 2-D tensor. One row has no pitch, and torch may report any for it."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+_NORMS = {None: 0, "layer": 1, "rms": 2}
+_MOD_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
+    """Pointer and row pitch of an optional 2-D tensor of the given shape and type."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype != dtype or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a {shape[0]} x {shape[1]} {dtype} tensor with unit column stride")
+    return t.data_ptr(), _ld(t)
+
+
+def _vector(t: Optional[torch.Tensor], name: str, cols: int):
+    if t is None:
+        return None
+    if t.shape != (cols,) or t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {cols} values")
+    return t.data_ptr()
+
+
+def _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches):
+    if x.dim() != 2 or x.dtype not in _MOD_DTYPES or x.stride(1) != 1:
+        raise ValueError("the stream must be a 2-D bf16 or float32 tensor with unit column stride")
+    if norm not in _NORMS:
+        raise ValueError('norm must be "layer", "rms" or None')
+    rows, cols = x.shape
+    mods = [m for m in (gate, scale, shift) if m is not None]
+    if offsets is not None:
+        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+            raise ValueError("offsets must be a contiguous 1-D int32 tensor of batches + 1 values")
+        if batches is not None and batches != offsets.shape[0] - 1:
+            raise ValueError("batches does not agree with offsets")
+        batches = offsets.shape[0] - 1
+    elif batches is None:
+        batches = mods[0].shape[0] if mods else 1
+    mod_dtype = mods[0].dtype if mods else torch.float32
+    if mod_dtype not in _MOD_DTYPES:
+        raise ValueError("gate, scale and shift must be bf16 or float32")
+    shape = (batches, cols)
+    pg, lg = _matrix(gate, "gate", shape, mod_dtype)
+    ps, ls = _matrix(scale, "scale", shape, mod_dtype)
+    ph, lh = _matrix(shift, "shift", shape, mod_dtype)
+    py, ly = _matrix(y, "y", x.shape, torch.bfloat16)
+    return _NormInputs(rows, cols, batches, _ptr(offsets), _OUT_KIND[x.dtype], _OUT_KIND[mod_dtype], _NORMS[norm],
+                       int(post_norm), residual_scale, eps, x.data_ptr(), _ld(x), py, ly, pg, lg, ps, ls, ph, lh,
+                       _vector(w_post, "w_post", cols), _vector(w, "w", cols))
+
+
+def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, hq: Optional[NVFP4Tensor] = None, *,
+                  y: Optional[torch.Tensor] = None, x_out: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, post_norm: bool = False,
+                  w_post: Optional[torch.Tensor] = None, residual_scale: float = 1.0, norm: Optional[str] = "layer",
+                  w: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  shift: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  offsets: Optional[torch.Tensor] = None, batches: Optional[int] = None,
+                  stats: Optional[torch.Tensor] = None, stream=None):
+    """x_out = residual_scale x + gate y~ (y~ = y or its RMSNorm), and the norm of x_out, modulated,
+    into h (bf16) and / or hq (NVFP4 with hq's static scale); see residual_norm in the header.
+
+    x, x_out: rows x cols, bf16 or float32; y: bf16. gate, scale, shift: batches x cols, bf16 or
+    float32 alike, possibly slices of one tensor. w, w_post: cols float32. offsets: batches + 1
+    int32 row offsets on the device (None: sequences of equal length); rows without a sequence are
+    left as they are. stats: rows x 4 float32, written for residual_norm_backward. Outputs that are
+    None are not written. Returns (x_out, h, hq)."""
+    dev = _same_device(x, h, y, x_out, gate, w_post, w, scale, shift, offsets, stats,
+                       *((hq.codes, hq.sf, hq.gscale) if hq is not None else ()))
+    a = _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
+    pxo, lxo = _matrix(x_out, "x_out", x.shape, x.dtype)
+    ph, lh = _matrix(h, "h", x.shape, torch.bfloat16)
+    _stats(stats, x.shape[0])
+    _call(load().residual_norm, "residual_norm", dev, stream, a, pxo, lxo, ph, lh,
+          ctypes.pointer(hq.c()) if hq is not None else None, _ptr(stats))
+    return x_out, h, hq
+
+
+def _stats(stats, rows):
+    if stats is not None and (stats.shape != (rows, 4) or stats.dtype != torch.float32 or not stats.is_contiguous()):
+        raise ValueError("stats must be a contiguous rows x 4 float32 tensor")
+
+
+def residual_norm_workspace_bytes(rows: int, cols: int, batches: int) -> int:
+    return int(load().residual_norm_workspace_bytes(rows, cols, batches))
+
+
+def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: Optional[torch.Tensor] = None,
+                           dh: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, post_norm: bool = False,
+                           w_post: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                           norm: Optional[str] = "layer", w: Optional[torch.Tensor] = None,
+                           scale: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                           offsets: Optional[torch.Tensor] = None, batches: Optional[int] = None,
+                           dx: Optional[torch.Tensor] = None, dy: Optional[torch.Tensor] = None,
+                           dgate: Optional[torch.Tensor] = None, dscale: Optional[torch.Tensor] = None,
+                           dshift: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                           dw_post: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> None:
+    """Gradient of residual_norm from those of its outputs (dx_out, dh; None: 0), into whichever of
+    dx, dy (as x, y), dgate, dscale, dshift (batches x cols float32), dw and dw_post (cols float32)
+    are given; they are overwritten. x_out is the stream that the forward call stored, stats what it
+    wrote there (see residual_norm_backward in the header)."""
+    seq = [t for t in (dgate, dscale, dshift) if t is not None]
+    dev = _same_device(x_out, stats, dx_out, dh, y, gate, w_post, w, scale, offsets, dx, dy, dgate, dscale, dshift,
+                       dw, dw_post, workspace)
+    if batches is None and offsets is None and gate is None and scale is None and seq:
+        batches = seq[0].shape[0]
+    a = _norm_inputs(x_out, y, gate, scale, None, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
+    _stats(stats, x_out.shape[0])
+    shape = (a.batches, a.cols)
+    g = _NormGrads(*_matrix(dx_out, "dx_out", x_out.shape, x_out.dtype), *_matrix(dh, "dh", x_out.shape, torch.bfloat16),
+                   *_matrix(dx, "dx", x_out.shape, x_out.dtype), *_matrix(dy, "dy", x_out.shape, torch.bfloat16),
+                   *_matrix(dgate, "dgate", shape, torch.float32), *_matrix(dscale, "dscale", shape, torch.float32),
+                   *_matrix(dshift, "dshift", shape, torch.float32), _vector(dw, "dw", a.cols),
+                   _vector(dw_post, "dw_post", a.cols))
+    if seq or dw is not None or dw_post is not None:
+        need = residual_norm_workspace_bytes(*x_out.shape, a.batches)
+        if workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        elif workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
+    _call(load().residual_norm_backward, "residual_norm_backward", dev, stream, a, stats.data_ptr(), g,
+          _ptr(workspace))
+
+
+def _rows_of_16_bytes(t: torch.Tensor) -> torch.Tensor:
+    """`t`, copied if its rows cannot be read 16 bytes at a time (a broadcast gradient, a view)."""
+    if t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] == 1 or (
+            t.stride(0) >= t.shape[1] and t.stride(0) * t.element_size() % 16 == 0)):
+        return t
+    return t.contiguous()
+
+
+class ResidualNorm(torch.autograd.Function):
+    """residual_norm with its gradient: apply(x, y, gate, scale, shift, w, w_post, norm, post_norm,
+    residual_scale, eps, offsets) returns (x_out, h); h alone without a branch (y None), x_out alone
+    with norm None. Rows without a sequence are 0 in the outputs and in the gradients. Parameters'
+    gradients are summed in float32 and returned in the parameter's type."""
+
+    @staticmethod
+    def forward(ctx, x, y=None, gate=None, scale=None, shift=None, w=None, w_post=None, norm="layer",
+                post_norm=False, residual_scale=1.0, eps=1e-6, offsets=None):
+        x, y, gate, scale, shift = (None if t is None else _rows_of_16_bytes(t) for t in (x, y, gate, scale, shift))
+        make = torch.empty if offsets is None else torch.zeros
+        x_out = make(x.shape, dtype=x.dtype, device=x.device) if y is not None else None
+        h = make(x.shape, dtype=torch.bfloat16, device=x.device) if norm is not None else None
+        stats = make((x.shape[0], 4), dtype=torch.float32, device=x.device)
+        mods = [m for m in (gate, scale, shift) if m is not None]
+        batches = mods[0].shape[0] if mods and offsets is None else None
+        residual_norm(x, h, y=y, x_out=x_out, gate=gate, post_norm=post_norm, w_post=w_post,
+                      residual_scale=residual_scale, norm=norm, w=w, scale=scale, shift=shift, eps=eps,
+                      offsets=offsets, batches=batches, stats=stats)
+        ctx.save_for_backward(x_out if y is not None else x, y, gate, scale, shift, w, w_post, offsets, stats)
+        ctx.args = (norm, post_norm, residual_scale, eps, batches)
+        ctx.set_materialize_grads(False)
+        if y is None:
+            return h
+        return (x_out, h) if norm is not None else x_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        x_out, y, gate, scale, shift, w, w_post, offsets, stats = ctx.saved_tensors
+        norm, post_norm, residual_scale, eps, batches = ctx.args
+        if y is None:
+            dx_out, dh = None, grads[0]
+        else:
+            dx_out, dh = grads if norm is not None else (grads[0], None)
+        if dx_out is None and dh is None:
+            return (None,) * 12
+        dx_out = None if dx_out is None else _rows_of_16_bytes(dx_out)
+        dh = None if dh is None else _rows_of_16_bytes(dh)
+        need = ctx.needs_input_grad
+        make = torch.empty_like if offsets is None else torch.zeros_like
+
+        def like(i, t):
+            return make(t, memory_format=torch.contiguous_format) if need[i] and t is not None else None
+
+        def sums(i, t):
+            return torch.empty(t.shape, dtype=torch.float32, device=t.device) if need[i] and t is not None else None
+
+        dx, dy = like(0, x_out), like(1, y)
+        dgate, dscale, dshift = sums(2, gate), sums(3, scale), sums(4, shift)
+        dw, dw_post = sums(5, w), sums(6, w_post)
+        if any(t is not None for t in (dx, dy, dgate, dscale, dshift, dw, dw_post)):
+            residual_norm_backward(x_out, stats, dx_out=dx_out, dh=dh, y=y, gate=gate, post_norm=post_norm,
+                                   w_post=w_post, residual_scale=residual_scale, norm=norm, w=w, scale=scale, eps=eps,
+                                   offsets=offsets, batches=batches, dx=dx, dy=dy, dgate=dgate, dscale=dscale,
+                                   dshift=dshift, dw=dw, dw_post=dw_post)
+
+        def cast(d, t):
+            return None if d is None else d.to(t.dtype)
+
+        return (dx, dy, cast(dgate, gate), cast(dscale, scale), cast(dshift, shift), dw, dw_post,
+                None, None, None, None, None)
+
+
+def rope_frequencies(pairs, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Frequencies of rope_axes: for an axis of n pairs, theta^(-j / n), j = 0 .. n - 1 (float64)."""
+    return torch.cat([theta ** (-torch.arange(n, dtype=torch.float64) / n) for n in pairs]).to(device)
+
+
+def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pairs, y: Optional[torch.Tensor] = None,
+              interleaved: bool = True, inverse: bool = False, stream=None) -> torch.Tensor:
+    """Rotary positions on heads x (rows x heads x head_dim; bf16, f16 or f32) into y, which may be
+    x itself (None: a new contiguous tensor). positions: rows x axes, int32 or float32; pairs: how
+    many pairs each axis turns; freqs: one float64 per pair (rope_frequencies). inverse: the
+    opposite rotation, which is also the gradient (see rope_axes in the header)."""
+    if x.dim() != 3 or x.dtype not in _OUT_KIND or x.stride(2) != 1:
+        raise ValueError("x must be a rows x heads x head_dim tensor (bf16, f16 or f32) with unit last stride")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif y.shape != x.shape or y.dtype != x.dtype or y.stride(2) != 1:
+        raise ValueError("y must have x's shape and type and unit last stride")
+    rows, heads, head_dim = x.shape
+    if positions.dim() != 2 or positions.shape != (rows, len(pairs)) or positions.dtype not in (
+            torch.int32, torch.float32) or (len(pairs) > 1 and positions.stride(1) != 1):
+        raise ValueError("positions must be rows x axes int32 or float32 with unit column stride")
+    if freqs.dtype != torch.float64 or freqs.shape != (sum(pairs),) or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 tensor with one value per pair")
+    dev = _same_device(x, y, positions, freqs)
+    ldpos = positions.stride(0) if rows > 1 else len(pairs)
+    _call(load().rope_axes, "rope_axes", dev, stream, x.data_ptr(), _OUT_KIND[x.dtype], rows, heads, head_dim,
+          x.stride(0), x.stride(1), positions.data_ptr(), int(positions.dtype == torch.float32), ldpos, len(pairs),
+          (ctypes.c_int32 * len(pairs))(*pairs), freqs.data_ptr(), int(interleaved), int(inverse), y.data_ptr(),
+          y.stride(0), y.stride(1))
+    return y
+
+
+class RopeAxes(torch.autograd.Function):
+    """rope_axes with its gradient (the opposite rotation): apply(x, positions, freqs, pairs,
+    interleaved). Positions and frequencies get none."""
+
+    @staticmethod
+    def forward(ctx, x, positions, freqs, pairs, interleaved=True):
+        ctx.save_for_backward(positions, freqs)
+        ctx.args = (tuple(pairs), interleaved)
+        return rope_axes(x, positions, freqs, pairs, interleaved=interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        positions, freqs = ctx.saved_tensors
+        pairs, interleaved = ctx.args
+        if dy.stride(2) != 1 or dy.data_ptr() % 16 or any(s * dy.element_size() % 16 for s in dy.stride()[:2]):
+            dy = dy.contiguous()
+        return rope_axes(dy, positions, freqs, pairs, interleaved=interleaved, inverse=True), None, None, None, None
 
 
 def read_device_status(stream=None) -> int:

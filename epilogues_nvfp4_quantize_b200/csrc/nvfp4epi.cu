@@ -16,6 +16,9 @@
 #include "quantize.cuh"
 #include "unfused.cuh"
 #include "gemm.cuh"
+#include "gemv.cuh"
+#include "residual_norm.cuh"
+#include "rope.cuh"
 
 #define NVFP4_API extern "C" __attribute__((visibility("default")))
 
@@ -39,6 +42,8 @@ struct DeviceInfo {
   // false>, <Y = true>
   int quant_ctas_per_sm[4] = {0, 0, 0, 0};
   int mx_ctas_per_sm[2] = {0, 0};  // resident CTAs of mx_quantize_kernel<V8 = false, true>
+  // clusters of gemv_nvfp4_kernel<NT = 1, 2> that fit at once, by log2 of the cluster size
+  int gemv_clusters[2][4] = {};
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mutex;
@@ -824,6 +829,451 @@ NVFP4_API nvfp4_status nvfp4_quantize_noalloc(const void* x, int64_t rows, int64
   nvfp4::quantize_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(
       xp, rows, cols, ldx, (flags & NVFP4_SWIGLU_INTERLEAVE) ? 1 : 0, amax_bits, out.gscale,
       static_cast<uint8_t*>(out.codes), static_cast<uint8_t*>(out.sf));
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return launch_status();
+}
+
+// -------------------------------------------------------------------------------------
+// Operators between the GEMMs of a layer: few-row products, residual norm, rotary positions.
+// -------------------------------------------------------------------------------------
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int64_t out_size(int dtype) { return dtype == NVFP4_OUT_F32 ? 4 : 2; }
+bool is_dtype(int d) { return d == NVFP4_OUT_BF16 || d == NVFP4_OUT_F16 || d == NVFP4_OUT_F32; }
+
+template <int NT>
+nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t stream) {
+  using namespace nvfp4::gemvcfg;
+  auto kern = nvfp4::gemv_nvfp4_kernel<NT>;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters[4];
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (info->gemv_clusters[NT - 1][0] == 0) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+      for (int i = 3; i >= 0; --i) {
+        attr[0].val.clusterDim.x = 1u << i;
+        cfg.gridDim = dim3(static_cast<unsigned>(info->sm_count >> i << i), 1, 1);
+        cfg.dynamicSmemBytes = MAX_SMEM;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return NVFP4_ERR_CUDA;
+        info->gemv_clusters[NT - 1][i] = n;
+      }
+    }
+    std::memcpy(clusters, info->gemv_clusters[NT - 1], sizeof(clusters));
+  }
+  // How K is cut: over the CTAs of a cluster (as far as x has to, to fit in shared memory, or to
+  // occupy the SMs when the weight has few rows) and over the warps of a CTA. The cost of a choice
+  // is the steps of its longest warp, plus about one step per join of warps and four per join of a
+  // cluster.
+  const int64_t groups = (a.K + GROUP - 1) / GROUP;
+  int64_t best = -1;
+  int best_i = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t slice = (groups + (1 << i) - 1) >> i;  // groups per CTA
+    if (slice * GROUP > (1 << 20) || nvfp4::gemv_smem(NT, static_cast<int>(slice * GROUP), 1 << i) > MAX_SMEM) continue;
+    if (i > 0 && slice * ((1 << i) - 1) >= groups) continue;  // a CTA without columns
+    for (int kw = 1; kw <= WARPS; kw <<= 1) {
+      const int64_t per_iter = static_cast<int64_t>(clusters[i]) * (WARPS / kw);
+      const int64_t iters = (a.strips + per_iter - 1) / per_iter;
+      const int64_t rounds = i == 0 ? 0 : (iters * (WARPS / kw) + ROUND - 1) / ROUND;
+      const int64_t cost = iters * ((slice + kw - 1) / kw + (kw > 1 ? 1 : 0)) + 4 * rounds;
+      if (best < 0 || cost < best) {
+        best = cost;
+        best_i = i;
+        a.kwarps = kw;
+      }
+    }
+  }
+  if (best < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  a.cluster = 1 << best_i;
+  a.kslice = static_cast<int>(((groups + a.cluster - 1) >> best_i) * GROUP);
+  const int64_t per_cluster = WARPS / a.kwarps;
+  int64_t n = (a.strips + per_cluster - 1) / per_cluster;
+  if (n > clusters[best_i]) n = clusters[best_i];
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(n * a.cluster), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)), 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(nvfp4::gemv_smem(NT, a.kslice, a.cluster));
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return launch_status();
+}
+
+}  // namespace
+
+NVFP4_API nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t ldx, int act, nvfp4_tensor B,
+                                  const float* bias, int out_dtype, void* D, int64_t ldd, cudaStream_t stream) {
+  if (x == nullptr || D == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (x_dtype != NVFP4_OUT_BF16 && x_dtype != NVFP4_OUT_F16) return NVFP4_ERR_INVALID_ARG;
+  if (act != NVFP4_ACT_NONE && act != NVFP4_ACT_SILU) return NVFP4_ERR_INVALID_ARG;
+  if (!is_dtype(out_dtype)) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status st;
+  if ((st = check_operand(B)) != NVFP4_OK) return st;
+  if (M <= 0 || M > (1ll << 19) || B.rows > (1ll << 31) || B.cols % 64 != 0 || B.cols > 32768)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (ldx < B.cols || ldd < B.rows) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(x) || ldx % 8 != 0 || !aligned_to(D, static_cast<uintptr_t>(out_size(out_dtype))) ||
+      !aligned_to(bias, 4) || !aligned_to(B.gscale, 4))
+    return NVFP4_ERR_MISALIGNED;
+  int dev;
+  DeviceInfo* info;
+  if ((st = current_device(&dev, &info)) != NVFP4_OK) return st;
+  nvfp4::GemvArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_f16 = x_dtype == NVFP4_OUT_F16;
+  a.ldx = ldx;
+  a.M = M;
+  a.N = B.rows;
+  a.K = B.cols;
+  a.silu = act == NVFP4_ACT_SILU;
+  a.codes = static_cast<const uint8_t*>(B.codes);
+  a.sf = static_cast<const uint8_t*>(B.sf);
+  a.gscale = B.gscale;
+  a.bias = bias;
+  a.D = D;
+  a.ldd = ldd;
+  a.out_kind = out_dtype;
+  a.strips = (B.rows + 127) / 128 * 8;
+  return M <= 8 ? launch_gemv<1>(info, a, stream) : launch_gemv<2>(info, a, stream);
+}
+
+namespace {
+
+// Checks that the forward call and the gradient share. `branch` and `norm` say which parts are used.
+nvfp4_status check_norm(const nvfp4_norm_inputs* in) {
+  if (in == nullptr || in->x == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (in->stream_dtype != NVFP4_OUT_BF16 && in->stream_dtype != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+  if (in->mod_dtype != NVFP4_OUT_BF16 && in->mod_dtype != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+  if (in->norm < NVFP4_NORM_NONE || in->norm > NVFP4_NORM_RMS) return NVFP4_ERR_INVALID_ARG;
+  if (in->post_norm != 0 && in->post_norm != 1) return NVFP4_ERR_INVALID_ARG;
+  if (!(in->eps > 0.0f) || !(in->eps <= 3.4028234663852886e38f)) return NVFP4_ERR_INVALID_ARG;
+  if (in->y == nullptr &&
+      (in->gate != nullptr || in->post_norm || in->w_post != nullptr || in->residual_scale != 1.0f))
+    return NVFP4_ERR_INVALID_ARG;
+  if (in->w_post != nullptr && !in->post_norm) return NVFP4_ERR_INVALID_ARG;
+  if (in->norm == NVFP4_NORM_NONE && (in->w != nullptr || in->scale != nullptr || in->shift != nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if (in->rows <= 0 || in->rows > (1ll << 31) - 256 || in->cols <= 0 || in->cols % 8 != 0 || in->cols > 16384 ||
+      in->batches <= 0 || in->batches > (1ll << 31))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (in->offsets == nullptr && in->rows % in->batches != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t st = out_size(in->stream_dtype), md = out_size(in->mod_dtype);
+  if (in->ldx < in->cols || (in->y != nullptr && in->ldy < in->cols)) return NVFP4_ERR_INVALID_ARG;
+  const struct {
+    const void* p;
+    int64_t ld;
+  } mods[3] = {{in->gate, in->ldgate}, {in->scale, in->ldscale}, {in->shift, in->ldshift}};
+  for (const auto& m : mods) {
+    if (m.p == nullptr) continue;
+    if (m.ld < in->cols) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(m.p) || (m.ld * md) % 16 != 0) return NVFP4_ERR_MISALIGNED;
+  }
+  if (!aligned16(in->x) || (in->ldx * st) % 16 != 0 || !aligned16(in->y) || (in->y != nullptr && in->ldy % 8 != 0) ||
+      !aligned16(in->w) || !aligned16(in->w_post) || !aligned_to(in->offsets, 4))
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+template <class ST>
+void launch_norm(const nvfp4::NormArgs& a, int64_t rows, cudaStream_t stream) {
+  const int64_t vecs = a.cols / 8;
+  if (vecs <= 128) {  // a warp per row, four rows per CTA
+    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+    if (vecs <= 32) {
+      nvfp4::residual_norm_kernel<ST, 1, true><<<grid, 128, 0, stream>>>(a);
+    } else if (vecs <= 64) {
+      nvfp4::residual_norm_kernel<ST, 2, true><<<grid, 128, 0, stream>>>(a);
+    } else {
+      nvfp4::residual_norm_kernel<ST, 4, true><<<grid, 128, 0, stream>>>(a);
+    }
+  } else {
+    const int threads = static_cast<int>((vecs + 63) / 64 * 32);
+    nvfp4::residual_norm_kernel<ST, 2, false><<<static_cast<unsigned>(rows), threads, 0, stream>>>(a);
+  }
+}
+
+template <class ST>
+void launch_norm_grad(const nvfp4::NormGradArgs& a, cudaStream_t stream) {
+  const int64_t vecs = a.cols / 8;
+  const unsigned grid = static_cast<unsigned>(a.chunks);
+  if (vecs <= 512) {
+    nvfp4::residual_norm_grad_kernel<ST, 1><<<grid, static_cast<int>((vecs + 31) / 32 * 32), 0, stream>>>(a);
+  } else if (vecs <= 1024) {
+    nvfp4::residual_norm_grad_kernel<ST, 2><<<grid, static_cast<int>((vecs + 63) / 64 * 32), 0, stream>>>(a);
+  } else {
+    nvfp4::residual_norm_grad_kernel<ST, 4><<<grid, static_cast<int>((vecs + 127) / 128 * 32), 0, stream>>>(a);
+  }
+}
+
+// Pieces that the rows are cut into for the gradient: two CTAs per SM of a B200 at 4096 columns, more
+// where a row keeps fewer threads busy.
+int64_t norm_chunks(int64_t rows, int64_t cols) {
+  const int64_t more = cols >= 4096 ? 1 : cols >= 2048 ? 2 : cols >= 1024 ? 4 : 8;
+  const int64_t n = 296 * more;
+  return rows < n ? rows : n;
+}
+
+}  // namespace
+
+NVFP4_API nvfp4_status residual_norm(const nvfp4_norm_inputs* in, void* x_out, int64_t ldxo, void* h, int64_t ldh,
+                                     const nvfp4_tensor* hq, float* stats, cudaStream_t stream) {
+  nvfp4_status st;
+  if ((st = check_norm(in)) != NVFP4_OK) return st;
+  if (x_out == nullptr && h == nullptr && hq == nullptr && stats == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (in->norm == NVFP4_NORM_NONE && (h != nullptr || hq != nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if ((x_out != nullptr && ldxo < in->cols) || (h != nullptr && ldh < in->cols)) return NVFP4_ERR_INVALID_ARG;
+  if (x_out == in->x && ldxo != in->ldx) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(x_out) || (x_out != nullptr && (ldxo * out_size(in->stream_dtype)) % 16 != 0) || !aligned16(h) ||
+      (h != nullptr && ldh % 8 != 0) || !aligned16(stats))
+    return NVFP4_ERR_MISALIGNED;
+  int64_t rows = in->rows;
+  if (hq != nullptr) {
+    if (hq->rows != in->rows || hq->cols != in->cols) return NVFP4_ERR_INVALID_ARG;
+    if ((st = check_operand(*hq)) != NVFP4_OK) return st;
+    if (in->cols % 64 != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    rows = (rows + 127) / 128 * 128;
+  }
+  int dev;
+  DeviceInfo* info;
+  if ((st = current_device(&dev, &info)) != NVFP4_OK) return st;
+  nvfp4::NormArgs a{};
+  a.rows = in->rows;
+  a.cols = in->cols;
+  a.batches = in->batches;
+  a.rows_per_batch = in->offsets == nullptr ? in->rows / in->batches : 1;
+  a.offsets = in->offsets;
+  a.x = in->x;
+  a.ldx = in->ldx;
+  a.y = static_cast<const uint16_t*>(in->y);
+  a.ldy = in->ldy;
+  a.gate = in->gate;
+  a.scale = in->scale;
+  a.shift = in->shift;
+  a.ldgate = in->ldgate;
+  a.ldscale = in->ldscale;
+  a.ldshift = in->ldshift;
+  a.mod_f32 = in->mod_dtype == NVFP4_OUT_F32;
+  a.post = in->post_norm;
+  a.w_post = in->w_post;
+  a.w = in->w;
+  a.norm = in->norm;
+  a.alpha = in->residual_scale;
+  a.eps = in->eps;
+  a.x_out = x_out;
+  a.ldxo = ldxo;
+  a.h = static_cast<uint16_t*>(h);
+  a.ldh = ldh;
+  if (hq != nullptr) {
+    a.q_codes = static_cast<uint8_t*>(hq->codes);
+    a.q_sf = static_cast<uint8_t*>(hq->sf);
+    a.q_gscale = hq->gscale;
+  }
+  a.stats = stats;
+  if (in->stream_dtype == NVFP4_OUT_F32) {
+    launch_norm<float>(a, rows, stream);
+  } else {
+    launch_norm<uint16_t>(a, rows, stream);
+  }
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return launch_status();
+}
+
+NVFP4_API int64_t residual_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t batches) {
+  if (rows <= 0 || cols <= 0 || batches <= 0) return -1;
+  const int64_t n = norm_chunks(rows, cols);
+  return ((n + batches) * 3 + n * 2) * cols * static_cast<int64_t>(sizeof(float));
+}
+
+NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const float* stats,
+                                              const nvfp4_norm_grads* g, void* workspace, cudaStream_t stream) {
+  nvfp4_status st;
+  if ((st = check_norm(in)) != NVFP4_OK) return st;
+  if (g == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (g->dx_out == nullptr && g->dh == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (g->dh != nullptr && in->norm == NVFP4_NORM_NONE) return NVFP4_ERR_INVALID_ARG;
+  if (stats == nullptr) return NVFP4_ERR_INVALID_ARG;
+  const bool seq = g->dgate != nullptr || g->dscale != nullptr || g->dshift != nullptr;
+  const bool weights = g->dw != nullptr || g->dw_post != nullptr;
+  if (g->dx == nullptr && g->dy == nullptr && !seq && !weights) return NVFP4_ERR_INVALID_ARG;
+  if (in->y == nullptr && (g->dy != nullptr || g->dgate != nullptr || g->dw_post != nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (g->dw_post != nullptr && !in->post_norm) return NVFP4_ERR_INVALID_ARG;
+  if (in->norm == NVFP4_NORM_NONE && (g->dscale != nullptr || g->dshift != nullptr || g->dw != nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if ((seq || weights) && workspace == nullptr) return NVFP4_ERR_INVALID_ARG;
+  const int64_t es = out_size(in->stream_dtype), cols = in->cols;
+  if ((g->dx_out != nullptr && g->lddxo < cols) || (g->dh != nullptr && g->lddh < cols) ||
+      (g->dx != nullptr && g->lddx < cols) || (g->dy != nullptr && g->lddy < cols) ||
+      (g->dgate != nullptr && g->lddgate < cols) || (g->dscale != nullptr && g->lddscale < cols) ||
+      (g->dshift != nullptr && g->lddshift < cols))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(stats) || !aligned16(g->dx_out) || (g->dx_out != nullptr && (g->lddxo * es) % 16 != 0) ||
+      !aligned16(g->dh) || (g->dh != nullptr && g->lddh % 8 != 0) || !aligned16(g->dx) ||
+      (g->dx != nullptr && (g->lddx * es) % 16 != 0) || !aligned16(g->dy) || (g->dy != nullptr && g->lddy % 8 != 0) ||
+      !aligned_to(g->dgate, 4) || !aligned_to(g->dscale, 4) || !aligned_to(g->dshift, 4) || !aligned_to(g->dw, 4) ||
+      !aligned_to(g->dw_post, 4) || !aligned16(workspace))
+    return NVFP4_ERR_MISALIGNED;
+  int dev;
+  DeviceInfo* info;
+  if ((st = current_device(&dev, &info)) != NVFP4_OK) return st;
+  nvfp4::NormGradArgs a{};
+  a.rows = in->rows;
+  a.cols = cols;
+  a.batches = in->batches;
+  a.rows_per_batch = in->offsets == nullptr ? in->rows / in->batches : 1;
+  a.offsets = in->offsets;
+  a.x = in->x;
+  a.ldx = in->ldx;
+  a.dxo = g->dx_out;
+  a.lddxo = g->lddxo;
+  a.dh = static_cast<const uint16_t*>(g->dh);
+  a.lddh = g->lddh;
+  a.y = static_cast<const uint16_t*>(in->y);
+  a.ldy = in->ldy;
+  a.gate = in->gate;
+  a.scale = in->scale;
+  a.ldgate = in->ldgate;
+  a.ldscale = in->ldscale;
+  a.mod_f32 = in->mod_dtype == NVFP4_OUT_F32;
+  a.post = in->post_norm;
+  a.w_post = in->w_post;
+  a.w = in->w;
+  a.norm = in->norm;
+  a.alpha = in->residual_scale;
+  a.stats = stats;
+  a.dx = g->dx;
+  a.lddx = g->lddx;
+  a.dy = static_cast<uint16_t*>(g->dy);
+  a.lddy = g->lddy;
+  a.dgate = g->dgate;
+  a.dscale = g->dscale;
+  a.dshift = g->dshift;
+  a.lddgate = g->lddgate;
+  a.lddscale = g->lddscale;
+  a.lddshift = g->lddshift;
+  a.dw = g->dw;
+  a.dw_post = g->dw_post;
+  a.chunks = static_cast<int>(norm_chunks(in->rows, cols));
+  if (seq || weights) {
+    a.seq_part = static_cast<float*>(workspace);
+    if (weights) a.w_part = a.seq_part + (a.chunks + in->batches) * 3 * cols;
+  }
+  if (in->stream_dtype == NVFP4_OUT_F32) {
+    launch_norm_grad<float>(a, stream);
+  } else {
+    launch_norm_grad<uint16_t>(a, stream);
+  }
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if ((st = launch_status()) != NVFP4_OK || !(seq || weights)) return st;
+  const int64_t by = !seq ? 0 : in->batches < 1024 ? in->batches : 1024;
+  const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(by + 1));
+  nvfp4::norm_grad_reduce_kernel<<<grid, 256, 0, stream>>>(a);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return launch_status();
+}
+
+namespace {
+
+template <class T>
+void launch_rope(const nvfp4::RopeArgs& a, bool interleaved, size_t smem, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
+  constexpr int T0 = nvfp4::ropecfg::THREADS;
+  if (interleaved) {
+    nvfp4::rope_kernel<T, nvfp4::ROPE_INTERLEAVED><<<grid, T0, smem, stream>>>(a);
+  } else if (a.npairs % nvfp4::RopeVec<T>::V == 0) {
+    nvfp4::rope_kernel<T, nvfp4::ROPE_HALVES><<<grid, T0, smem, stream>>>(a);
+  } else {  // the second half does not start on 16 bytes
+    nvfp4::rope_kernel<T, nvfp4::ROPE_HALVES_SCALAR><<<grid, T0, smem, stream>>>(a);
+  }
+}
+
+}  // namespace
+
+NVFP4_API nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t heads, int64_t head_dim,
+                                 int64_t x_row_stride, int64_t x_head_stride, const void* positions, int pos_float,
+                                 int64_t ldpos, int axes, const int32_t* pairs, const double* freqs, int interleaved,
+                                 int inverse, void* y, int64_t y_row_stride, int64_t y_head_stride,
+                                 cudaStream_t stream) {
+  using namespace nvfp4::ropecfg;
+  if (x == nullptr || y == nullptr || positions == nullptr || pairs == nullptr || freqs == nullptr)
+    return NVFP4_ERR_INVALID_ARG;
+  if (!is_dtype(dtype) || (pos_float & ~1) || (interleaved & ~1) || (inverse & ~1)) return NVFP4_ERR_INVALID_ARG;
+  if (rows <= 0 || rows > (1ll << 31) - 1 || heads <= 0 || heads > (1 << 16) || head_dim <= 0 || head_dim % 8 != 0 ||
+      head_dim > MAX_HEAD_DIM || axes < 1 || axes > MAX_AXES)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  int64_t n = 0;
+  nvfp4::RopeArgs a{};
+  for (int i = 0; i < MAX_AXES; ++i) {
+    if (i < axes) {
+      if (pairs[i] < 1 || pairs[i] > head_dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+      n += pairs[i];
+    }
+    a.axis_end[i] = i < axes - 1 ? static_cast<int>(n) : 0x7fffffff;
+  }
+  if (2 * n > head_dim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (ldpos < axes) return NVFP4_ERR_INVALID_ARG;
+  // heads of y must not share elements (those of x may: a broadcast input)
+  const bool rows_outer = y_row_stride >= y_head_stride;
+  const int64_t inner = rows_outer ? y_head_stride : y_row_stride, outer = rows_outer ? y_row_stride : y_head_stride;
+  const int64_t inner_n = rows_outer ? heads : rows, outer_n = rows_outer ? rows : heads;
+  if ((inner_n > 1 && inner < head_dim) ||
+      (outer_n > 1 && (outer < head_dim || (inner_n > 1 && outer / inner < inner_n - 1) ||
+                       (inner_n > 1 && outer < (inner_n - 1) * inner + head_dim))))
+    return NVFP4_ERR_INVALID_ARG;
+  if (x_row_stride < 0 || x_head_stride < 0) return NVFP4_ERR_INVALID_ARG;
+  if (x == y && ((rows > 1 && x_row_stride != y_row_stride) || (heads > 1 && x_head_stride != y_head_stride)))
+    return NVFP4_ERR_INVALID_ARG;
+  const int64_t es = out_size(dtype);
+  if (!aligned16(x) || !aligned16(y) || (rows > 1 && ((x_row_stride * es) % 16 != 0 || (y_row_stride * es) % 16 != 0)) ||
+      (heads > 1 && ((x_head_stride * es) % 16 != 0 || (y_head_stride * es) % 16 != 0)) || !aligned_to(freqs, 8) ||
+      !aligned_to(positions, 4))
+    return NVFP4_ERR_MISALIGNED;
+  int dev;
+  DeviceInfo* info;
+  nvfp4_status st;
+  if ((st = current_device(&dev, &info)) != NVFP4_OK) return st;
+  a.x = x;
+  a.y = y;
+  a.rows = rows;
+  a.heads = static_cast<int>(heads);
+  a.head_dim = static_cast<int>(head_dim);
+  a.x_row = x_row_stride;
+  a.x_head = x_head_stride;
+  a.y_row = y_row_stride;
+  a.y_head = y_head_stride;
+  a.pos = positions;
+  a.pos_f32 = pos_float;
+  a.ldpos = ldpos;
+  a.freqs = freqs;
+  a.npairs = static_cast<int>(n);
+  a.inverse = inverse;
+  a.in_place = x == y;
+  // rows per CTA: about two batches of 16-byte accesses per thread, a table within its limit, and
+  // enough CTAs for the GPU
+  int64_t r = 2 * BATCH * THREADS * 16 / (heads * head_dim * es);
+  const int64_t table = MAX_TABLE_BYTES / (n * 8);
+  if (r > table) r = table;
+  if (r > rows / (8 * info->sm_count)) r = rows / (8 * info->sm_count);
+  if (r < 1) r = 1;
+  a.rows_per_cta = static_cast<int>(r);
+  const size_t smem = static_cast<size_t>(r * n) * sizeof(float2);
+  const bool inter = interleaved != 0;
+  if (dtype == NVFP4_OUT_F32) {
+    launch_rope<float>(a, inter, smem, stream);
+  } else if (dtype == NVFP4_OUT_F16) {
+    launch_rope<__half>(a, inter, smem, stream);
+  } else {
+    launch_rope<__nv_bfloat16>(a, inter, smem, stream);
+  }
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return launch_status();
 }

@@ -1,0 +1,631 @@
+// residual_norm: the residual stream between two blocks of a layer, and its gradient.
+//
+//   x' = alpha x + gate[b] y~        y~ = y, or y rsqrt(mean y^2 + eps) w_post
+//   h  = n(x') w (1 + scale[b]) + shift[b],   n = LayerNorm or RMSNorm over the row
+//
+// b is the row's sequence (a modulation vector each). x' is rounded to the stream's type once,
+// and the norm reads the rounded value: the gradient, which only has the stored x', then
+// differentiates exactly what was computed. h is rounded to bf16 once; its NVFP4 form quantises
+// those bf16 values, as every re-quantised output of this library does.
+// Sums, means and reciprocal roots are float32; the variance is taken from centred values (a
+// second pass over registers), so a mean much larger than the spread costs no digits.
+#pragma once
+
+#include "ptx.cuh"
+#include "codec.cuh"
+
+namespace nvfp4 {
+
+struct NormArgs {
+  int64_t rows, cols;
+  int64_t batches;        // sequences
+  int64_t rows_per_batch; // of each sequence, when offsets is null
+  const int* offsets;     // batches + 1 row offsets, or null
+  const void* x;          // the stream (bf16 or float32)
+  int64_t ldx;
+  const uint16_t* y;      // the branch (bf16), or null
+  int64_t ldy;
+  const void* gate;       // batches x cols (bf16 or float32, see mod_f32), or null (1)
+  const void* scale;      // or null (0)
+  const void* shift;      // or null (0)
+  int64_t ldgate, ldscale, ldshift;
+  int mod_f32;
+  int post;               // RMSNorm on the branch
+  const float* w_post;    // or null (1)
+  const float* w;         // or null (1)
+  int norm;               // 0 none, 1 LayerNorm, 2 RMSNorm
+  float alpha, eps;
+  void* x_out;            // or null
+  int64_t ldxo;
+  uint16_t* h;            // or null
+  int64_t ldh;
+  uint8_t* q_codes;       // NVFP4 output, or null
+  uint8_t* q_sf;
+  const float* q_gscale;
+  float* stats;           // rows x 4: mean, rstd, rstd of the branch, 0; or null
+};
+
+enum NormKind { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
+
+// Sequence of a row, or -1 when it has none (rows before the first offset or behind the last).
+// The offsets come from the device and are not checked: whatever they hold, the answer is -1
+// or in [0, batches).
+__device__ __forceinline__ int64_t norm_sequence(const int* offsets, int64_t batches, int64_t rows_per_batch,
+                                                 int64_t row) {
+  if (offsets == nullptr) return row / rows_per_batch;
+  int64_t lo = 0, hi = batches + 1;  // number of offsets <= row
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(__ldg(offsets + mid)) <= row) {
+      lo = mid + 1;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo > batches ? -1 : lo - 1;
+}
+
+// Eight values of the stream.
+template <class ST>
+struct Stream8;
+template <>
+struct Stream8<uint16_t> {
+  uint4 q;
+  __device__ void load(const void* base, int64_t at) {
+    q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+  }
+  __device__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  // Rounds v to the stream's type (in place) and holds the result.
+  __device__ void round(float (&v)[8]) {
+    q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+    get(v);
+  }
+  __device__ void store(void* base, int64_t at) const {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = q;
+  }
+};
+template <>
+struct Stream8<float> {
+  float4 q[2];
+  __device__ void load(const void* base, int64_t at) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    q[0] = p[0];
+    q[1] = p[1];
+  }
+  __device__ void get(float (&v)[8]) const {
+    v[0] = q[0].x, v[1] = q[0].y, v[2] = q[0].z, v[3] = q[0].w;
+    v[4] = q[1].x, v[5] = q[1].y, v[6] = q[1].z, v[7] = q[1].w;
+  }
+  __device__ void round(float (&v)[8]) {
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ void store(void* base, int64_t at) const {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    p[0] = q[0];
+    p[1] = q[1];
+  }
+};
+
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, float (&v)[8]) {
+  Stream8<uint16_t> s;
+  s.load(p, 0);
+  s.get(v);
+}
+
+// Eight modulation values at column c of sequence b.
+__device__ __forceinline__ void load8_mod(const void* base, int mod_f32, int64_t at, float (&v)[8]) {
+  if (mod_f32) {
+    Stream8<float> s;
+    s.load(base, at);
+    s.get(v);
+  } else {
+    Stream8<uint16_t> s;
+    s.load(base, at);
+    s.get(v);
+  }
+}
+__device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
+  Stream8<float> s;
+  s.load(p, 0);
+  s.get(v);
+}
+
+// Sum over the threads of a row: one warp (ONE_WARP), or all of the CTA's (red: 32 floats,
+// flipped between two halves by the caller so that one barrier per sum suffices).
+template <bool ONE_WARP>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (ONE_WARP) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// One row per CTA (ONE_WARP: per warp); thread t holds the eight columns at 8 t, and with NV > 1
+// those at 8 (t + i threads).
+template <class ST, int NV, bool ONE_WARP>
+__global__ void __launch_bounds__(ONE_WARP ? 128 : 1024) residual_norm_kernel(const NormArgs a) {
+  __shared__ float red[3][32];
+  const int threads = ONE_WARP ? 32 : blockDim.x;
+  const int t = ONE_WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t row = ONE_WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                               : static_cast<int64_t>(blockIdx.x);
+  const int64_t nkb = a.cols >> 4;
+  if (row >= a.rows) {  // rows that pad the block scales to 128 (their scales are 0)
+    if (a.q_codes != nullptr && row < ((a.rows + 127) & ~int64_t(127))) {
+      for (int64_t g = t; g < (a.cols >> 6); g += threads)
+        *reinterpret_cast<uint32_t*>(a.q_sf + sf_word_offset(row, 4 * g, nkb)) = 0u;
+    }
+    return;
+  }
+  const int64_t b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
+  if (b < 0) return;
+
+  Stream8<ST> xs[NV];
+  float v[NV][8];
+  uint4 yq[NV];
+  bool live[NV];
+  int64_t col[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    col[i] = 8 * static_cast<int64_t>(t + i * threads);
+    live[i] = col[i] < a.cols;
+    if (live[i]) {
+      xs[i].load(a.x, row * a.ldx + col[i]);
+      if (a.y != nullptr) yq[i] = *reinterpret_cast<const uint4*>(a.y + row * a.ldy + col[i]);
+    }
+  }
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  float rstd_y = 1.0f;
+  if (a.y != nullptr) {
+    if (a.post) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live[i]) continue;
+        const uint32_t w[4] = {yq[i].x, yq[i].y, yq[i].z, yq[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ss = fmaf(bf16_lo(w[k]), bf16_lo(w[k]), fmaf(bf16_hi(w[k]), bf16_hi(w[k]), ss));
+      }
+      rstd_y = rsqrtf(row_sum<ONE_WARP>(ss, red[0]) * inv_n + a.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      float g[8], yv[8];
+      Stream8<uint16_t> ys;
+      ys.q = yq[i];
+      ys.get(yv);
+      xs[i].get(v[i]);
+      if (a.post) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) yv[k] *= rstd_y;
+        if (a.w_post != nullptr) {
+          load8_f32(a.w_post + col[i], g);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) yv[k] *= g[k];
+        }
+      }
+      if (a.gate != nullptr) {
+        load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) yv[k] *= g[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = fmaf(a.alpha, v[i][k], yv[k]);
+      xs[i].round(v[i]);
+      if (a.x_out != nullptr) xs[i].store(a.x_out, row * a.ldxo + col[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      xs[i].get(v[i]);
+      if (a.x_out != nullptr) xs[i].store(a.x_out, row * a.ldxo + col[i]);
+    }
+  }
+  float mean = 0.0f, rstd = 1.0f;
+  if (a.norm != NORM_NONE) {
+    if (a.norm == NORM_LAYER) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live[i]) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[i][k];
+      }
+      mean = row_sum<ONE_WARP>(s, red[1]) * inv_n;
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[i][k] -= mean;
+        ss = fmaf(v[i][k], v[i][k], ss);
+      }
+    }
+    rstd = rsqrtf(row_sum<ONE_WARP>(ss, red[2]) * inv_n + a.eps);
+  }
+  if (a.stats != nullptr && t == 0) *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(mean, rstd, rstd_y, 0.0f);
+  if (a.norm == NORM_NONE) return;
+
+  float G = 0.0f, enc = 0.0f;
+  if (a.q_codes != nullptr) {
+    G = *a.q_gscale;
+    enc = scale_encode_factor(G);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    Stream8<uint16_t> out;
+    out.q = make_uint4(0u, 0u, 0u, 0u);
+    if (live[i]) {
+      float g[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] *= rstd;
+      if (a.w != nullptr) {
+        load8_f32(a.w + col[i], g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] *= g[k];
+      }
+      if (a.scale != nullptr) {
+        load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = fmaf(v[i][k], g[k], v[i][k]);
+      }
+      if (a.shift != nullptr) {
+        load8_mod(a.shift, a.mod_f32, b * a.ldshift + col[i], g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] += g[k];
+      }
+      out.round(v[i]);
+      if (a.h != nullptr) out.store(a.h, row * a.ldh + col[i]);
+    }
+    if (a.q_codes != nullptr) {
+      // a block of 16 is two lanes, a scale word (64 columns) eight: cols % 64 == 0, so each
+      // group of eight lanes is live as a whole
+      float amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, live[i] ? fabsf(v[i][k]) : 0.0f);
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      const uint32_t s = block_scale_code(amax, enc);
+      const float r = block_inv_scale(s, G);
+      const int lane = threadIdx.x & 31;
+      uint32_t word = (lane & 1) ? 0u : s << (4 * (lane & 7));
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      if (live[i]) {
+        const uint32_t codes = r > 0.0f ? block_codes8(v[i], r) : 0u;
+        *reinterpret_cast<uint32_t*>(a.q_codes + row * (a.cols >> 1) + (col[i] >> 1)) = codes;
+        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.q_sf + sf_word_offset(row, col[i] >> 4, nkb)) = word;
+      }
+    }
+  }
+}
+
+// =====================================================================================
+// Gradient. With xhat = (x' - mean) rstd, d = dh w (1 + scale), yh the normalised branch (or y):
+//   T       = dx' + rstd (d - mean(d) [LayerNorm] - xhat mean(d xhat))     gradient of x'
+//   dx      = alpha T
+//   dy      = gate T, or with the branch's norm rstd_y (a - yh mean(a yh)), a = gate w_post T
+//   dshift  = sum_b dh,  dscale = sum_b dh xhat w,  dgate = sum_b T yh w_post
+//   dw      = sum dh xhat (1 + scale),  dw_post = sum gate T yh
+// so three sums over a sequence's rows (dh, dh xhat, T yh) give every parameter's gradient.
+// mean(a yh) depends on T; it is expanded into sums that do not (six row sums in all), so that a
+// row needs one reduction only.
+//
+// Rows are cut into `chunks` contiguous pieces, one CTA each; a thread keeps its columns and
+// adds up the three sums in registers over the rows of its piece. Where a sequence ends, the sums
+// go to slot chunk + sequence of the workspace (that index grows with every piece, so no two
+// pieces share one); norm_grad_reduce_kernel adds a sequence's slots in their order. No atomics:
+// the same inputs give the same bits.
+// =====================================================================================
+struct NormGradArgs {
+  int64_t rows, cols, batches, rows_per_batch;
+  const int* offsets;
+  const void* x;          // x', the stored stream
+  int64_t ldx;
+  const void* dxo;        // gradient of x' from what follows (the stream's type), or null (0)
+  int64_t lddxo;
+  const uint16_t* dh;     // or null: no norm
+  int64_t lddh;
+  const uint16_t* y;      // or null: no branch
+  int64_t ldy;
+  const void* gate;
+  const void* scale;
+  int64_t ldgate, ldscale;
+  int mod_f32;
+  int post;
+  const float* w_post;
+  const float* w;
+  int norm;
+  float alpha;
+  const float* stats;
+  void* dx;
+  int64_t lddx;
+  uint16_t* dy;
+  int64_t lddy;
+  float* dgate;           // batches x cols, or null; likewise below
+  float* dscale;
+  float* dshift;
+  int64_t lddgate, lddscale, lddshift;
+  float* dw;              // cols, or null
+  float* dw_post;
+  int chunks;
+  float* seq_part;        // (chunks + batches) x 3 x cols, or null (no sums)
+  float* w_part;          // chunks x 2 x cols, or null (neither dw nor dw_post)
+};
+
+__device__ __forceinline__ int64_t norm_chunk_row(int64_t rows, int chunks, int64_t g) { return rows * g / chunks; }
+
+// Sums of six values per thread over the CTA (blockDim.x a multiple of 32): every thread gets
+// all six. `red` holds 32 x 8 floats.
+__device__ __forceinline__ void cta_sum6(float (&s)[6], float* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 6; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) red[warp * 8 + k] = s[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 6; ++k) {
+    s[k] = lane < warps ? red[lane * 8 + k] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  }
+}
+
+template <class ST, int NV>
+__global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormGradArgs a) {
+  __shared__ float red[2][32 * 8];
+  const int g = blockIdx.x;
+  const int64_t r0 = norm_chunk_row(a.rows, a.chunks, g), r1 = norm_chunk_row(a.rows, a.chunks, g + 1);
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  bool live[NV];
+  int64_t col[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    col[i] = 8 * static_cast<int64_t>(threadIdx.x + i * blockDim.x);
+    live[i] = col[i] < a.cols;
+  }
+  float s_dh[NV][8], s_dhx[NV][8], s_ty[NV][8];  // sums over the current sequence's rows
+  float cw[NV][8], gt[NV][8];                     // w (1 + scale) and the gate, of the sequence
+  bool first_flush = true;
+  int64_t b = -1, seq_end = r0;
+
+  auto flush = [&]() {
+    if (a.seq_part == nullptr) return;  // no sums are asked for
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      float* p = a.seq_part + (g + b) * 3 * a.cols + col[i];
+      const float* const src[3] = {s_dh[i], s_dhx[i], s_ty[i]};
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        *reinterpret_cast<float4*>(p + k * a.cols) = make_float4(src[k][0], src[k][1], src[k][2], src[k][3]);
+        *reinterpret_cast<float4*>(p + k * a.cols + 4) = make_float4(src[k][4], src[k][5], src[k][6], src[k][7]);
+      }
+      if (a.w_part != nullptr) {
+        float* q = a.w_part + static_cast<int64_t>(g) * 2 * a.cols + col[i];
+        float sc[8];
+        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], sc);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float one = a.scale != nullptr ? 1.0f + sc[k] : 1.0f;
+          const float w0 = one * s_dhx[i][k], p0 = gt[i][k] * s_ty[i][k];
+          q[k] = first_flush ? w0 : q[k] + w0;
+          q[a.cols + k] = first_flush ? p0 : q[a.cols + k] + p0;
+        }
+      }
+    }
+    first_flush = false;
+  };
+
+  int parity = 0;
+  for (int64_t row = r0; row < r1; ++row) {
+    if (row >= seq_end) {
+      if (b >= 0) flush();
+      b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
+      if (b < 0) {  // rows without a sequence are left as they are
+        seq_end = row + 1;
+        continue;
+      }
+      seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          s_dh[i][k] = s_dhx[i][k] = s_ty[i][k] = 0.0f;
+          cw[i][k] = gt[i][k] = 1.0f;
+        }
+        if (!live[i]) continue;
+        if (a.scale != nullptr) {
+          load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], cw[i]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) cw[i][k] += 1.0f;
+        }
+        if (a.w != nullptr) {
+          float w[8];
+          load8_f32(a.w + col[i], w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) cw[i][k] *= w[k];
+        }
+        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], gt[i]);
+      }
+    }
+    const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * row);
+    const float mean = st.x, rstd = st.y, rstd_y = a.post ? st.z : 1.0f;
+    float xh[NV][8], d[NV][8], t[NV][8], yh[NV][8], ag[NV][8];
+    float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) xh[i][k] = d[i][k] = t[i][k] = yh[i][k] = ag[i][k] = 0.0f;
+      if (!live[i]) continue;
+      Stream8<ST> v;
+      if (a.dxo != nullptr) {
+        v.load(a.dxo, row * a.lddxo + col[i]);
+        v.get(t[i]);
+      }
+      if (a.y != nullptr) {
+        load8_bf16(a.y + row * a.ldy + col[i], yh[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) yh[i][k] *= rstd_y;
+      }
+      if (a.dh != nullptr) {
+        v.load(a.x, row * a.ldx + col[i]);
+        v.get(xh[i]);
+        load8_bf16(a.dh + row * a.lddh + col[i], d[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          xh[i][k] = (xh[i][k] - mean) * rstd;
+          s_dh[i][k] += d[i][k];
+          s_dhx[i][k] = fmaf(d[i][k], xh[i][k], s_dhx[i][k]);
+          d[i][k] *= cw[i][k];
+          s[0] += d[i][k];
+          s[1] = fmaf(d[i][k], xh[i][k], s[1]);
+        }
+      }
+      if (a.post) {
+        float wp[8];
+        if (a.w_post != nullptr) load8_f32(a.w_post + col[i], wp);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          ag[i][k] = a.w_post != nullptr ? gt[i][k] * wp[k] : gt[i][k];
+          const float ay = ag[i][k] * yh[i][k];
+          s[2] = fmaf(ay, t[i][k], s[2]);
+          s[3] = fmaf(ay, d[i][k], s[3]);
+          s[4] += ay;
+          s[5] = fmaf(ay, xh[i][k], s[5]);
+        }
+      }
+    }
+    cta_sum6(s, red[parity]);
+    parity ^= 1;
+    const float m1 = a.norm == NORM_LAYER ? s[0] * inv_n : 0.0f, m2 = s[1] * inv_n;
+    const float m3 = a.post ? (s[2] + rstd * (s[3] - m1 * s[4] - m2 * s[5])) * inv_n : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (a.dh != nullptr) t[i][k] = fmaf(rstd, d[i][k] - m1 - xh[i][k] * m2, t[i][k]);
+        s_ty[i][k] = fmaf(t[i][k], yh[i][k], s_ty[i][k]);
+        o[k] = a.alpha * t[i][k];
+      }
+      if (a.dx != nullptr) {
+        Stream8<ST> v;
+        v.round(o);
+        v.store(a.dx, row * a.lddx + col[i]);
+      }
+      if (a.dy != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          o[k] = a.post ? rstd_y * (ag[i][k] * t[i][k] - yh[i][k] * m3) : gt[i][k] * t[i][k];
+        Stream8<uint16_t> v;
+        v.round(o);
+        v.store(a.dy, row * a.lddy + col[i]);
+      }
+    }
+  }
+  if (b >= 0) flush();
+  if (a.w_part != nullptr && first_flush) {  // none of this piece's rows has a sequence
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      for (int k = 0; k < 8; ++k) {
+        a.w_part[static_cast<int64_t>(g) * 2 * a.cols + col[i] + k] = 0.0f;
+        a.w_part[(static_cast<int64_t>(g) * 2 + 1) * a.cols + col[i] + k] = 0.0f;
+      }
+    }
+  }
+}
+
+// Adds up the slots of each sequence and the pieces' weight sums. Block (x, y): columns 32 x and
+// on; y < gridDim.y - 1 takes the sequences y, y + gridDim.y - 1, ..., the last y the weights.
+// Eight rows of threads share the slots and are joined in a fixed order.
+__global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArgs a) {
+  __shared__ float red[3][8][33];
+  const int cx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + cx;
+  const bool live = col < a.cols;
+  auto join = [&](int k, float v) { red[k][ty][cx] = v; };
+  auto total = [&](int k) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += red[k][i][cx];
+    return v;
+  };
+  if (blockIdx.y == gridDim.y - 1) {
+    float s0 = 0.0f, s1 = 0.0f;
+    if (live && a.w_part != nullptr) {
+      for (int g = ty; g < a.chunks; g += 8) {
+        s0 += a.w_part[static_cast<int64_t>(g) * 2 * a.cols + col];
+        s1 += a.w_part[(static_cast<int64_t>(g) * 2 + 1) * a.cols + col];
+      }
+    }
+    join(0, s0);
+    join(1, s1);
+    __syncthreads();
+    if (ty == 0 && live) {
+      if (a.dw != nullptr) a.dw[col] = total(0);
+      if (a.dw_post != nullptr) a.dw_post[col] = total(1);
+    }
+    return;
+  }
+  for (int64_t b = blockIdx.y; b < a.batches; b += gridDim.y - 1) {
+    int64_t s = a.offsets == nullptr ? b * a.rows_per_batch : static_cast<int64_t>(a.offsets[b]);
+    int64_t e = a.offsets == nullptr ? s + a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
+    if (s < 0) s = 0;
+    if (e > a.rows) e = a.rows;
+    float v[3] = {0.0f, 0.0f, 0.0f};
+    if (s < e) {
+      // pieces that hold rows of [s, e): the first one found from an estimate, then in order
+      int64_t g0 = s * a.chunks / a.rows;
+      while (g0 > 0 && norm_chunk_row(a.rows, a.chunks, g0) > s) --g0;
+      while (norm_chunk_row(a.rows, a.chunks, g0 + 1) <= s) ++g0;
+      for (int64_t g = g0 + ty; g < a.chunks && norm_chunk_row(a.rows, a.chunks, g) < e; g += 8) {
+        if (norm_chunk_row(a.rows, a.chunks, g + 1) == norm_chunk_row(a.rows, a.chunks, g) || !live) continue;
+        const float* p = a.seq_part + (g + b) * 3 * a.cols + col;
+        v[0] += p[0];
+        v[1] += p[a.cols];
+        v[2] += p[2 * a.cols];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) join(k, v[k]);
+    __syncthreads();
+    if (ty == 0 && live) {
+      if (a.dshift != nullptr) a.dshift[b * a.lddshift + col] = total(0);
+      if (a.dscale != nullptr) a.dscale[b * a.lddscale + col] = a.w != nullptr ? total(1) * a.w[col] : total(1);
+      if (a.dgate != nullptr) {
+        const float v2 = total(2);
+        a.dgate[b * a.lddgate + col] = a.post && a.w_post != nullptr ? v2 * a.w_post[col] : v2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace nvfp4

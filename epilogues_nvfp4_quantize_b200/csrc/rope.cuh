@@ -1,0 +1,227 @@
+// rope_axes: rotary positions with one to four axes (time, height, width) on heads of Q and K.
+//
+// Pair p of a head belongs to one axis a(p) and has a frequency f_p. With the row's position
+// t_a on that axis, the pair (u, v) becomes (u cos A - v sin A, u sin A + v cos A),
+// A = t_a(p) f_p; the inverse (and the gradient) is the same with -A. HBM-bound: every element is
+// read and written once (plus the positions).
+//
+// Angles: A grows with the position while only A mod 2 pi matters, so t f and its reduction are
+// in float64 (a float32 product at t = 10^6 is off by 0.06 rad); the reduced angle, at most pi,
+// goes to sincospif in float32 (error about 2e-7). All heads of a row share its angles, so a CTA
+// computes them once into shared memory and then walks its rows' heads with 16-byte accesses.
+#pragma once
+
+#include "ptx.cuh"
+#include "codec.cuh"
+
+namespace nvfp4 {
+
+namespace ropecfg {
+constexpr int THREADS = 256;
+constexpr int BATCH = 4;        // heads in flight per thread
+constexpr int MAX_AXES = 4;
+constexpr int MAX_HEAD_DIM = 1024;
+constexpr int MAX_TABLE_BYTES = 16384;  // cos/sin pairs of a CTA's rows
+}  // namespace ropecfg
+
+enum RopeMode { ROPE_INTERLEAVED = 0, ROPE_HALVES = 1, ROPE_HALVES_SCALAR = 2 };
+
+struct RopeArgs {
+  const void* x;
+  void* y;
+  int64_t rows;
+  int heads, head_dim;
+  int64_t x_row, x_head, y_row, y_head;  // strides in elements
+  const void* pos;
+  int pos_f32;                           // positions are float32 (else int32)
+  int64_t ldpos;
+  const double* freqs;                   // npairs, in radians per position
+  int npairs;                            // rotated pairs; elements past 2 * npairs pass through
+  int axis_end[ropecfg::MAX_AXES];       // axis a holds pairs [axis_end[a-1], axis_end[a])
+  int inverse;
+  int rows_per_cta;
+  int in_place;                          // y is x: what passes through stays where it is
+};
+
+template <class T>
+struct RopeVec;  // 16 bytes of T as floats
+template <>
+struct RopeVec<float> {
+  static constexpr int V = 4;
+  __device__ static void unpack(const uint4& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x);
+    v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z);
+    v[3] = __uint_as_float(q.w);
+  }
+  __device__ static uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct RopeVec<__nv_bfloat16> {
+  static constexpr int V = 8;
+  __device__ static void unpack(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  __device__ static uint4 pack(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  }
+};
+template <>
+struct RopeVec<__half> {
+  static constexpr int V = 8;
+  __device__ static void unpack(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ static uint4 pack(const float (&v)[8]) {
+    return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                      pack_f16x2(v[6], v[7]));
+  }
+};
+
+__device__ __forceinline__ float rope_f32(float v) { return v; }
+__device__ __forceinline__ float rope_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float rope_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ void rope_put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void rope_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void rope_put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// cos and sin of the pairs of this CTA's rows. `width` entries per row; those past npairs are
+// not read.
+__device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int nrows, float2* cs) {
+  for (int i = threadIdx.x; i < nrows * a.npairs; i += ropecfg::THREADS) {
+    const int r = i / a.npairs, p = i - r * a.npairs;
+    int ax = 0;
+#pragma unroll
+    for (int k = 0; k < ropecfg::MAX_AXES - 1; ++k) ax += p >= a.axis_end[k] ? 1 : 0;
+    const int64_t at = (row0 + r) * a.ldpos + ax;
+    const double t = a.pos_f32 ? static_cast<double>(static_cast<const float*>(a.pos)[at])
+                               : static_cast<double>(static_cast<const int*>(a.pos)[at]);
+    double u = t * a.freqs[p] * 0.31830988618379067154;  // in units of pi
+    u -= 2.0 * rint(0.5 * u);
+    float s, c;
+    sincospif(static_cast<float>(u), &s, &c);
+    cs[i] = make_float2(c, a.inverse ? -s : s);
+  }
+}
+
+// A unit is what one thread does to one head: 16 bytes (interleaved pairs), two times 16 bytes
+// (the same places of both halves) or a 16-byte piece that passes through, and with
+// ROPE_HALVES_SCALAR (a number of pairs that 16 bytes do not divide) one pair or one element.
+// Threads keep their unit and walk the (row, head) pairs of the CTA.
+template <class T, int MODE>
+__global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a) {
+  using namespace ropecfg;
+  using RV = RopeVec<T>;
+  constexpr int V = RV::V;
+  extern __shared__ float2 rope_cs[];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
+  const int nrows = static_cast<int>(a.rows - row0 < a.rows_per_cta ? a.rows - row0 : a.rows_per_cta);
+  rope_table(a, row0, nrows, rope_cs);
+  __syncthreads();
+
+  const int n = a.npairs;
+  const int units = MODE == ROPE_INTERLEAVED ? a.head_dim / V
+                    : MODE == ROPE_HALVES    ? n / V + (a.head_dim - 2 * n) / V
+                                             : a.head_dim - n;
+  const int slots = units < THREADS ? THREADS / units : 1;
+  const int slot = units < THREADS ? threadIdx.x / units : 0;
+  if (slot >= slots) return;
+  const int total = nrows * a.heads;
+  for (int u = threadIdx.x - slot * units; u < units; u += THREADS) {
+    const bool rotates = MODE == ROPE_INTERLEAVED ? u * (V / 2) < n : MODE == ROPE_HALVES ? u * V < n : u < n;
+    if (!rotates && a.in_place) continue;
+    // first element of the unit within the head
+    const int e0 = MODE == ROPE_INTERLEAVED ? u * V
+                   : MODE == ROPE_HALVES    ? (rotates ? u * V : 2 * n + (u - n / V) * V)
+                                            : (rotates ? u : n + u);
+    int r = slot / a.heads, h = slot - (slot / a.heads) * a.heads;
+    for (int j = slot; j < total; j += BATCH * slots) {
+      const T* src[BATCH];
+      T* dst[BATCH];
+      const float2* cs[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        src[k] = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + h * a.x_head + e0;
+        dst[k] = static_cast<T*>(a.y) + (row0 + r) * a.y_row + h * a.y_head + e0;
+        cs[k] = rope_cs + r * n;
+        h += slots;
+        while (h >= a.heads) {
+          h -= a.heads;
+          ++r;
+        }
+      }
+      if constexpr (MODE == ROPE_HALVES_SCALAR) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          if (j + k * slots >= total) continue;
+          if (!rotates) {
+            *dst[k] = *src[k];
+          } else {
+            const float p = rope_f32(src[k][0]), q = rope_f32(src[k][n]);
+            const float2 c = cs[k][u];
+            rope_put(dst[k], p * c.x - q * c.y);
+            rope_put(dst[k] + n, p * c.y + q * c.x);
+          }
+        }
+      } else {
+        uint4 lo[BATCH], hi[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          if (j + k * slots < total) {
+            lo[k] = *reinterpret_cast<const uint4*>(src[k]);
+            if (MODE == ROPE_HALVES && rotates) hi[k] = *reinterpret_cast<const uint4*>(src[k] + n);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          if (j + k * slots >= total) continue;
+          if (rotates) {
+            float v[V];
+            RV::unpack(lo[k], v);
+            if constexpr (MODE == ROPE_INTERLEAVED) {
+#pragma unroll
+              for (int i = 0; i < V / 2; ++i) {
+                const int p = u * (V / 2) + i;
+                if (p < n) {
+                  const float2 c = cs[k][p];
+                  const float s0 = v[2 * i], s1 = v[2 * i + 1];
+                  v[2 * i] = s0 * c.x - s1 * c.y;
+                  v[2 * i + 1] = s0 * c.y + s1 * c.x;
+                }
+              }
+            } else {
+              float w[V];
+              RV::unpack(hi[k], w);
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                const float2 c = cs[k][u * V + i];
+                const float s0 = v[i], s1 = w[i];
+                v[i] = s0 * c.x - s1 * c.y;
+                w[i] = s0 * c.y + s1 * c.x;
+              }
+              *reinterpret_cast<uint4*>(dst[k] + n) = RV::pack(w);
+            }
+            lo[k] = RV::pack(v);
+          }
+          *reinterpret_cast<uint4*>(dst[k]) = lo[k];
+        }
+      }
+    }
+  }
+}
+
+}  // namespace nvfp4

@@ -292,6 +292,146 @@ nvfp4_status swiglu_bf16(const void* c, int64_t rows, int64_t nh, int64_t ldc,
                          void* y, int64_t ldy, cudaStream_t stream);
 
 /*
+ * A few rows of activations times an NVFP4 weight (the conditioning vectors of a layer's
+ * modulation, the timestep embedding, the tokens of a decoding step): the row counts that the
+ * GEMMs above, which take 128 rows and quantise both operands, do not serve. The weight stays in
+ * the layout of those GEMMs' B operand; the activations stay in 16 bits.
+ *   D[m, n] = cast(G sum_k f(x[m, k]) e2m1(codes[n, k]) e4m3(sf[n, k / 16]) + bias[n])
+ *   x: M x K of x_dtype (NVFP4_OUT_BF16 or NVFP4_OUT_F16), leading dimension ldx.
+ *   act: NVFP4_ACT_NONE (f the identity) or NVFP4_ACT_SILU (f(x) = x / (1 + exp(-x)), rounded to
+ *        x's type as a separate kernel would leave it).
+ *   bias: N float32, or NULL.  D: M x N of out_dtype, leading dimension ldd elements.
+ * Products are exact and sums float32; x is held in f16 scaled by a power of two per row, which is
+ * exact for every value down to 2^-28 of the row's largest finite one and off by at most 2^-39 of
+ * that below. Infinities and NaN in x reach the outputs of their row only.
+ * Rules: M >= 1 (rows are taken 16 at a time: past 16, the weight is read again for each 16 rows),
+ *        N >= 1, K % 64 == 0, K <= 32768 (UNSUPPORTED_SHAPE); ldx >= K, ldd >= N (INVALID_ARG);
+ *        x and ldx*2 bytes, codes and sf 16-byte aligned, bias and gscale 4-byte aligned, D
+ *        aligned to its element (MISALIGNED).
+ */
+#define NVFP4_ACT_SILU 2
+nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t ldx, int act, nvfp4_tensor B,
+                        const float* bias, int out_dtype, void* D, int64_t ldd, cudaStream_t stream);
+
+/*
+ * The residual stream between two blocks of a layer: the branch's output, normalised or not, is
+ * gated and added to the stream, and the next block's input is normalised and modulated, in one
+ * pass and one launch.
+ *   x' = residual_scale x + gate[b] y~     y~ = y, or with post_norm y rsqrt(mean(y^2) + eps) w_post
+ *   h  = n(x') w (1 + scale[b]) + shift[b]
+ * n is LayerNorm ((x' - mean) rsqrt(var + eps), var the mean square of the centred row) or RMSNorm
+ * (x' rsqrt(mean(x'^2) + eps)). x' is rounded to the stream's type, and n reads the rounded values.
+ * h is rounded to bf16; hq quantises those bf16 values with the static scale *hq->gscale, as
+ * nvfp4_quantize with compute_amax = 0 would: it is the A operand of the next GEMM.
+ *   x, x_out : rows x cols of stream_dtype (NVFP4_OUT_BF16 or NVFP4_OUT_F32). x_out may be x, or
+ *              NULL.
+ *   y        : rows x cols bf16, or NULL: no branch (then x' = x, residual_scale must be 1 and
+ *              gate, post_norm, w_post are not given).
+ *   gate, scale, shift : batches x cols of mod_dtype (NVFP4_OUT_BF16 or NVFP4_OUT_F32), each with
+ *              its leading dimension, or NULL (1, 0 and 0). They may be slices of one tensor.
+ *   w_post, w: cols float32, or NULL (1).
+ *   norm     : NVFP4_NORM_NONE (x' only), NVFP4_NORM_LAYER or NVFP4_NORM_RMS.
+ *   offsets  : NULL (sequence b is rows [b rows / batches, (b + 1) rows / batches), rows a multiple
+ *              of batches), or a DEVICE array of batches + 1 non-decreasing int32 row offsets:
+ *              sequence b is rows [offsets[b], offsets[b + 1]). Rows before the first and behind
+ *              the last offset are left as they are in every output. The kernels stay in bounds
+ *              whatever the array holds.
+ *   h, hq    : bf16 and NVFP4 outputs; either may be NULL (NORM_NONE: both).
+ *   stats    : rows x 4 float32 (mean, rstd, rstd of the branch, 0) for the gradient, or NULL.
+ * Rules: rows >= 1, cols % 8 == 0 (cols % 64 == 0 with hq), cols <= 16384, 1 <= batches
+ *        (UNSUPPORTED_SHAPE); eps > 0 and finite; every pointer and row pitch 16-byte aligned
+ *        (offsets 4). Outputs may not overlap inputs, except x_out == x with the same pitch.
+ */
+#define NVFP4_NORM_NONE 0
+#define NVFP4_NORM_LAYER 1
+#define NVFP4_NORM_RMS 2
+typedef struct {
+  int64_t rows, cols, batches;
+  const int32_t* offsets;
+  int stream_dtype, mod_dtype;
+  int norm, post_norm;
+  float residual_scale, eps;
+  const void* x;
+  int64_t ldx;
+  const void* y;
+  int64_t ldy;
+  const void* gate;
+  int64_t ldgate;
+  const void* scale;
+  int64_t ldscale;
+  const void* shift;
+  int64_t ldshift;
+  const float* w_post;
+  const float* w;
+} nvfp4_norm_inputs;
+
+nvfp4_status residual_norm(const nvfp4_norm_inputs* in, void* x_out, int64_t ldxo, void* h, int64_t ldh,
+                           const nvfp4_tensor* hq, float* stats, cudaStream_t stream);
+
+/*
+ * Gradient of residual_norm. `in` as in the forward call, except that in->x is x', the stream that
+ * call stored (its x_out); in->shift is not read. `stats` is what the forward call wrote.
+ *   dx_out : gradient of x' from what follows (stream_dtype), or NULL (0).
+ *   dh     : gradient of h (bf16), or NULL (then the norm contributes nothing).
+ *   Outputs, each of which may be NULL: dx (stream_dtype), dy (bf16); dgate, dscale, dshift
+ *   (batches x cols float32, sums over a sequence's rows); dw, dw_post (cols float32, sums over all
+ *   rows that have a sequence). They are overwritten, not added to. A sequence without rows gets 0.
+ * The sums are float32, over pieces of rows and then over the pieces in order: the same inputs give
+ * the same bits.
+ *   workspace: residual_norm_workspace_bytes(rows, cols, batches) bytes, 16-byte aligned, contents
+ *              ignored on entry; calls that share one must not overlap on the GPU. It may be NULL
+ *              when none of dgate, dscale, dshift, dw and dw_post is asked for.
+ * Rules as residual_norm; dx may be dx_out (same pitch), dy may be dh or y.
+ */
+typedef struct {
+  const void* dx_out;
+  int64_t lddxo;
+  const void* dh;
+  int64_t lddh;
+  void* dx;
+  int64_t lddx;
+  void* dy;
+  int64_t lddy;
+  float* dgate;
+  int64_t lddgate;
+  float* dscale;
+  int64_t lddscale;
+  float* dshift;
+  int64_t lddshift;
+  float* dw;
+  float* dw_post;
+} nvfp4_norm_grads;
+
+int64_t residual_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t batches);
+nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const float* stats, const nvfp4_norm_grads* g,
+                                    void* workspace, cudaStream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height and width of a video's tokens; height and width
+ * of an image's; one axis for text) on heads of Q and K, for instance those that
+ * gemm_nvfp4_rmsnorm left in the QKV buffer.
+ * A head's first 2 P elements are P pairs; axis a owns the next `pairs[a]` of them in order
+ * (P their sum). Pair p of axis a turns by the angle positions[row, a] * freqs[p]:
+ *   (u, v) -> (u cos - v sin, u sin + v cos);   inverse = 1 turns by the negative angle, which is
+ *   also the gradient of the rotation.
+ *   interleaved = 1: pair p is elements 2 p and 2 p + 1; 0: elements p and P + p. Elements from
+ *   2 P on are copied.
+ *   x, y   : rows x heads x head_dim of dtype (NVFP4_OUT_*), unit stride inside a head, the others
+ *            given in elements. y may be x with the same strides (in place).
+ *   positions: rows x axes of int32 (pos_float = 0) or float32 (1), row pitch ldpos.
+ *   freqs  : P float64 on the device, radians per position (angles are formed in float64, so far
+ *            positions keep their digits).
+ * Rules: rows, heads >= 1, head_dim a multiple of 8 and <= 1024, 1 <= axes <= 4, pairs[a] >= 1,
+ *        2 P <= head_dim (UNSUPPORTED_SHAPE); y's heads may not overlap one another, ldpos >= axes
+ *        (INVALID_ARG); x, y and all their strides 16-byte aligned, freqs 8, positions 4
+ *        (MISALIGNED). y may not overlap x otherwise. `pairs` is a HOST array.
+ */
+nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t heads, int64_t head_dim, int64_t x_row_stride,
+                       int64_t x_head_stride, const void* positions, int pos_float, int64_t ldpos, int axes,
+                       const int32_t* pairs, const double* freqs, int interleaved, int inverse, void* y,
+                       int64_t y_row_stride, int64_t y_head_stride, cudaStream_t stream);
+
+/*
  * Allocation-free variant of nvfp4_quantize with compute_amax = 1. This entry point has no
  * counterpart on the page; it exists for callers that cannot allocate device memory: code
  * embedded in a host application that owns the whole GPU and hands out only its own
