@@ -362,28 +362,29 @@ class FakeQuantizeSTE(torch.autograd.Function):
 
 
 # ---- operators between the GEMMs of a layer -------------------------------------------
-def _same_device(*tensors: Optional[torch.Tensor]) -> torch.device:
-    """The one CUDA device that all given tensors are on."""
-    dev = None
+def _same_device(*tensors: Optional[torch.Tensor]) -> int:
+    """Index of the one CUDA device that all given tensors are on."""
+    dev = -2
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors must be on one device")
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    raise ValueError("tensors must be on a CUDA device")
+                if dev != -2:
+                    raise ValueError("tensors must be on one device")
+                dev = i
     return dev
 
 
-def _call(fn, what: str, dev: torch.device, stream, *args) -> None:
+def _call(fn, what: str, dev: int, stream, *args) -> None:
     """Call `fn` with `dev` current (the library launches on the current device), on `stream` or
     on that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == dev.index:
+        stream = torch._C._cuda_getCurrentRawStream(dev)  # current_stream() would build an object: 2 us
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -537,7 +538,7 @@ def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: 
     if seq or dw is not None or dw_post is not None:
         need = residual_norm_workspace_bytes(*x_out.shape, a.batches)
         if workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = torch.empty((need,), dtype=torch.uint8, device=x_out.device)
         elif workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
     _call(load().residual_norm_backward, "residual_norm_backward", dev, stream, a, stats.data_ptr(), g,

@@ -25,6 +25,8 @@
 
 #include "ptx.cuh"
 #include "codec.cuh"
+#include "quantize.cuh"
+#include "unfused.cuh"
 
 namespace nvfp4 {
 
@@ -34,6 +36,7 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int GROUP = 128;            // columns of K per step of a warp
 constexpr int TILE_TOKENS = 16;       // rows of x per pass over the weight
 constexpr int ROUND = 16;             // strips between two joins of a cluster
+constexpr int SLOT = 32 * (2 * 16 + 2 * 4);  // bytes of a step in shared memory: 16 + 16 of codes, 4 + 4 of scales a lane
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_SMEM = 220 * 1024;
 }  // namespace gemvcfg
@@ -52,25 +55,48 @@ struct GemvArgs {
   int64_t ldd;
   int out_kind;          // NVFP4_OUT_*
   int kslice;            // columns of K per CTA of a cluster (a multiple of GROUP)
-  int cluster;           // CTAs that share K
-  int kwarps;            // warps that share a CTA's slice (a power of two)
-  int64_t strips;
+  int cluster_log2;      // log2 of the CTAs that share K
+  int kwarps_log2;       // log2 of the warps that share a CTA's slice
+  int per;               // steps of each of those warps
+  int strips;
+  int strips_at_once;    // of the whole grid
+  int iters;             // strips each warp takes
 };
 
 __host__ __device__ constexpr int gemv_x_pitch(int kslice) { return kslice * 2 + 64; }  // bytes per row of x
-__host__ __device__ constexpr int gemv_smem(int nt, int kslice, int cluster) {
-  return 8 * nt * gemv_x_pitch(kslice) + 2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? gemvcfg::ROUND * 512 * nt : 0) +
-         8 * nt * 4 + 64 * 4;
+__host__ __device__ constexpr int gemv_smem(int nt, int depth, int64_t tokens, int kslice, int cluster) {
+  return gemvcfg::WARPS * depth * gemvcfg::SLOT +                                                // ring of weights
+         2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? gemvcfg::ROUND * 512 * nt : 0) +         // joins
+         8 * nt * 8 +                                                                            // row factors
+         static_cast<int>(tokens < 8 * nt ? tokens : 8 * nt) * gemv_x_pitch(kslice);             // x
 }
 
-__device__ __forceinline__ float gemv_act(float v, int silu) {
-  return silu ? v / (1.0f + expf(-v)) : v;
+__device__ __forceinline__ void gemv_unpack(const uint4& q, int f16, float (&f)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (f16) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    } else {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
 }
 
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 c;\n\tcvt.u8.u32 c, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(byte));
-  return r;
+// Eight E2M1 codes to four f16 pairs, in their order. Taking the bytes apart inside the PTX costs
+// about one instruction per pair; shifting and masking them out first was measured at four.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t c, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(c));
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -84,165 +110,260 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ void mma_16x8x16_from0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                  uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Barrier of `threads` threads, by its id (0 is __syncthreads).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
+// Asynchronous copies to shared memory; bytes past `n` of the 16 or 4 are written as 0.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_async16_hint(uint32_t dst, const void* src, int n, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(n),
+               "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-// One step's codes and scales of a lane: 32 columns of rows n0 and n1.
-struct GemvStep {
-  uint4 c[2];
-  uint32_t s[2];  // two E4M3 codes each
-};
-
-template <int NT>
+// DEPTH (a power of two): steps of codes and scales in flight per warp.
+template <int NT, int DEPTH>
 __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const GemvArgs a) {
   using namespace gemvcfg;
   extern __shared__ __align__(128) uint8_t gemv_smem_raw[];
+  const int cluster = 1 << a.cluster_log2, kwarps = 1 << a.kwarps_log2;
   const int pitch = gemv_x_pitch(a.kslice);
-  uint8_t* xs = gemv_smem_raw;
-  float* red = reinterpret_cast<float*>(xs + 8 * NT * pitch);   // [2][WARPS][32][4 NT]
-  float* part = red + 2 * WARPS * 128 * NT;                      // [ROUND][32][4 NT] (clusters)
-  float* inv = part + (a.cluster > 1 ? ROUND * 128 * NT : 0);    // factor of each row of x
+  uint8_t* ring = gemv_smem_raw;                                               // [WARPS][DEPTH][SLOT]
+  float* red = reinterpret_cast<float*>(ring + WARPS * DEPTH * SLOT);          // [2][WARPS][32][4 NT]
+  float* part = red + 2 * WARPS * 128 * NT;                                    // [ROUND][32][4 NT] (clusters)
+  float* inv = part + (cluster > 1 ? ROUND * 128 * NT : 0);                    // factor of each row of x
   unsigned* amax = reinterpret_cast<unsigned*>(inv + 8 * NT);
+  uint8_t* xs = reinterpret_cast<uint8_t*>(amax + 8 * NT);                     // [tokens][pitch]
 
+  griddep_launch_dependents();
+  griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rank = static_cast<int>(blockIdx.x) % a.cluster;
-  const int64_t cid = blockIdx.x / a.cluster, ncluster = gridDim.x / a.cluster;
-  const int64_t k0 = static_cast<int64_t>(rank) * a.kslice;
-  const int64_t kleft = a.K - k0;
-  const int klen = static_cast<int>(kleft < 0 ? 0 : kleft < a.kslice ? kleft : a.kslice);  // a multiple of 64
+  const int rank = static_cast<int>(blockIdx.x) & (cluster - 1);
+  const int cid = static_cast<int>(blockIdx.x) >> a.cluster_log2;
+  const int k0 = rank * a.kslice;
+  const int kleft = static_cast<int>(a.K) - k0;
+  const int klen = kleft < 0 ? 0 : kleft < a.kslice ? kleft : a.kslice;  // a multiple of 64
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
   const int tokens = static_cast<int>(a.M - m0 < 8 * NT ? a.M - m0 : 8 * NT);
 
-  // ---- this slice of x into shared memory as f16, each row by its power of two ----------
-  if (tid < 8 * NT) amax[tid] = 0u;
-  __syncthreads();
-  const int vecs = klen >> 3;
-  auto load_x = [&](int m, int v, float (&f)[8]) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (m0 + m) * a.ldx + k0 + 8 * v));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (a.x_f16) {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = h.x;
-        f[2 * i + 1] = h.y;
-      } else {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-      }
-    }
-    if (a.silu) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = gemv_act(f[i], 1);
-        f[i] = a.x_f16 ? __half2float(__float2half_rn(f[i])) : __bfloat162float(__float2bfloat16_rn(f[i]));
-      }
-    }
+  // ---- this slice of x on its way into shared memory -------------------------------------
+  // Columns 32 t + 8 w .. + 7 of a group sit at 64 w + 16 t bytes of it. Each row is taken by as
+  // many warps as there are (one at least); a thread comes back to the same vectors in each pass.
+  const int vecs = klen >> 3, xvecs = a.kslice >> 3;
+  const int xwarps_log2 = tokens <= 1 ? 4 : tokens <= 2 ? 3 : tokens <= 4 ? 2 : tokens <= 8 ? 1 : 0;
+  const int xm = warp >> xwarps_log2;
+  auto each_vector = [&](auto&& body) {
+    if (xm >= tokens) return;
+    uint8_t* row = xs + xm * pitch;
+    for (int v = ((warp & ((1 << xwarps_log2) - 1)) << 5) + lane; v < xvecs; v += 32 << xwarps_log2)
+      body(v, reinterpret_cast<uint4*>(row + (v >> 4) * 256 + (v & 3) * 64 + ((v >> 2) & 3) * 16));
   };
-  // Pass 1: the largest finite magnitude of each row (a row has a multiple of 8 vectors, so the
-  // eight lanes of an octet share a row). Pass 2 reads the slice again from L2.
-  for (int i = tid; i < tokens * vecs; i += THREADS) {
-    const int m = i / vecs;
-    float f[8], big = 0.0f;
-    load_x(m, i - m * vecs, f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float z = fabsf(f[k]);
-      if (z <= 3.4028234663852886e38f) big = fmaxf(big, z);
-    }
-    const uint32_t octet = 0xFFu << (lane & 24);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(octet, big, o));
-    if ((lane & 7) == 0) atomicMax(amax + m, __float_as_uint(big));
+  {
+    const uint16_t* row = a.x + (m0 + xm) * a.ldx + k0;
+    each_vector([&](int v, uint4* p) { copy_async16(smem_u32(p), v < vecs ? row + 8 * v : a.x, v < vecs ? 16 : 0); });
   }
-  __syncthreads();
-  const int xvecs = a.kslice / 8;
-  for (int i = tid; i < 8 * NT * xvecs; i += THREADS) {
-    const int m = i / xvecs, v = i - m * xvecs;
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (m < tokens) {
-      // the row's factor 2^(14 - e) and its inverse; the clamp keeps both normal float32 numbers
-      int e = static_cast<int>(amax[m] >> 23) - 127;
-      if (e < -100) e = -100;
-      if (v == 0) inv[m] = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
-      if (v < vecs) {
-        const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+  copy_async_commit();
+  if (tid < 8 * NT) amax[tid] = 0u;
+  const float G = *a.gscale;
+
+  // ---- the walk over weights: step = one 128-column group of one strip ---------------------
+  // Every warp takes `per` groups of each of its strips (groups past the slice are skipped), so the
+  // warps of a strip reach its join together. A lane copies its own bytes of the coming DEPTH steps
+  // into its own places of a ring in shared memory, so nothing but its own cp.async groups has to be
+  // waited for. (Loads into registers kept 2 steps in flight in the 128 registers a thread has:
+  // 27.0 us on 2 x 4096 x 24576, bound by the latency of DRAM.)
+  const int wk = warp & (kwarps - 1), wr = warp >> a.kwarps_log2, rows_at_once = WARPS >> a.kwarps_log2;
+  const int groups = (klen + GROUP - 1) / GROUP;
+  const int gb = wk * a.per;
+  const int64_t krow = a.K >> 1;  // bytes of codes per weight row
+
+  // The next step to load. Rows past N and strips past the last load the last ones again: their
+  // results are not stored. Columns past the slice become 0.
+  int l_strip = cid * rows_at_once + wr;
+  int l_step = 0;
+  int l_left;  // columns of the slice from the lane's first one on
+  const uint8_t *l_codes0, *l_codes1, *l_sf;
+  auto seek = [&]() {
+    const int64_t s = l_strip < a.strips ? l_strip : a.strips - 1;
+    const int64_t tile = s >> 3;
+    const int r = static_cast<int>(s & 7) * 4 + (g & 3);
+    const int64_t n0 = tile * 128 + (g >> 2) * 32 + r, n1 = n0 + 64;
+    const int k = k0 + gb * GROUP + 32 * t;
+    l_left = klen - gb * GROUP - 32 * t;
+    l_codes0 = a.codes + (n0 < a.N ? n0 : a.N - 1) * krow + (k >> 1);
+    l_codes1 = a.codes + (n1 < a.N ? n1 : a.N - 1) * krow + (k >> 1);
+    l_sf = a.sf + (tile * (a.K >> 6) + (k >> 6)) * 512 + r * 16 + (g >> 2) * 4;
+  };
+  // codes are read once per call: they leave L2 first, so that x and what else is used again stay
+  const uint64_t once = l2_policy_evict_first();
+  const uint32_t my_ring = smem_u32(ring) + warp * (DEPTH * SLOT);
+  auto load = [&](uint32_t slot) {
+    if (l_strip < a.strips) {
+      const int n = l_left > 0 ? 16 : 0;  // past the slice nothing is read
+      const uint32_t c = slot + lane * 16, f = slot + 1024 + lane * 4;
+      copy_async16_hint(c, l_codes0, n, once);
+      copy_async16_hint(c + 512, l_codes1, n, once);
+      copy_async4(f, l_sf, n >> 2);
+      copy_async4(f + 128, l_sf + 8, n >> 2);
+      l_left -= GROUP;
+      l_codes0 += GROUP / 2;
+      l_codes1 += GROUP / 2;
+      l_sf += 1024;
+      if (++l_step == a.per) {
+        l_step = 0;
+        l_strip += a.strips_at_once;
+        seek();
+      }
+    }
+    copy_async_commit();
+  };
+  seek();
+#pragma unroll
+  for (int j = 0; j < DEPTH; ++j) load(my_ring + j * SLOT);
+
+  // ---- x to f16, each row by its power of two ---------------------------------------------
+  copy_async_wait<DEPTH>();
+  if (a.x_f16 && !a.silu) {  // f16 needs no factor
+    if (tid < 8 * NT) inv[tid] = 1.0f;
+  } else {
+    __syncthreads();  // amax is 0
+    // Pass 1: f(x) as it is stored (16 bits), and the largest finite magnitude of each row.
+    float big = 0.0f;
+    each_vector([&](int v, uint4* p) {
+      uint4 q = *p;
+      if (a.silu) {
         float f[8];
-        load_x(m, v, f);
+        gemv_unpack(q, a.x_f16, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = silu_f32(f[k]);
+        q = a.x_f16 ? make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                                 pack_f16x2(f[6], f[7]))
+                    : make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                 pack_bf16x2(f[6], f[7]));
+        *p = q;
+      }
+      float f[8];
+      gemv_unpack(q, a.x_f16, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float z = fabsf(f[k]);
+        big = fmaxf(big, z <= 3.4028234663852886e38f ? z : 0.0f);
+      }
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    if (lane == 0 && xm < tokens) atomicMax(amax + xm, __float_as_uint(big));
+    __syncthreads();
+    // Pass 2: to f16, by the row's factor 2^(14 - e); the clamp keeps it and its inverse normal
+    // float32 numbers.
+    if (xm < tokens) {
+      int e = static_cast<int>(amax[xm] >> 23) - 127;
+      if (e < -100) e = -100;
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      if (lane == 0) inv[xm] = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+      each_vector([&](int, uint4* p) {
+        float f[8];
+        gemv_unpack(*p, a.x_f16, f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] *= up;
-        o = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
-      }
-    } else if (v == 0) {
-      inv[m] = 0.0f;
+        *p = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+      });
     }
-    // columns 32 t + 8 w .. + 7 of a group sit at 64 w + 16 t bytes of it
-    *reinterpret_cast<uint4*>(xs + m * pitch + (v >> 4) * 256 + (v & 3) * 64 + ((v >> 2) & 3) * 16) = o;
   }
   __syncthreads();
 
-  // ---- strips ---------------------------------------------------------------------------
-  const int wk = warp & (a.kwarps - 1), wr = warp / a.kwarps, rows_at_once = WARPS / a.kwarps;
-  const int groups = a.kslice / GROUP;
-  const int per = (groups + a.kwarps - 1) / a.kwarps;
-  const int gb = wk * per, ge = gb + per < groups ? gb + per : groups;  // this warp's groups of the slice
-  const float G = *a.gscale;
-  const int64_t kgroups64 = a.K >> 6;
-
-  auto load_step = [&](int64_t tile, int r, int64_t n0, int grp, GemvStep& st) {
-    const int64_t k = k0 + static_cast<int64_t>(grp) * GROUP + 32 * t;
-    st.c[0] = st.c[1] = make_uint4(0u, 0u, 0u, 0u);
-    st.s[0] = st.s[1] = 0u;
-    if (k < a.K) {
-      const uint8_t* sp = a.sf + (tile * kgroups64 + (k >> 6)) * 512 + (r * 4 + (g >> 2)) * 4 + ((k >> 4) & 3);
-      const uint8_t* cp = a.codes + n0 * (a.K >> 1) + (k >> 1);
-      if (n0 < a.N) {
-        st.c[0] = __ldg(reinterpret_cast<const uint4*>(cp));
-        st.s[0] = __ldg(reinterpret_cast<const uint16_t*>(sp));
-      }
-      if (n0 + 64 < a.N) {
-        st.c[1] = __ldg(reinterpret_cast<const uint4*>(cp + 64 * (a.K >> 1)));
-        st.s[1] = __ldg(reinterpret_cast<const uint16_t*>(sp + 8));
-      }
-    }
-  };
+  // ---- products -------------------------------------------------------------------------
+  // The accumulator of the tensor core is off by more per addition than a rounded float32 sum; it
+  // only runs over one step (128 columns), and the steps are added in float32.
   float acc[NT][4];
-  auto compute = [&](int grp, const GemvStep& st) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  const uint8_t* xlane[NT];  // rows past the tokens read the last one: their columns are not stored
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xlane[n] = xs + (8 * n + g < tokens ? 8 * n + g : tokens - 1) * pitch + gb * 256 + t * 16;
+  auto compute = [&](int step, const uint8_t* slot) {
     uint32_t s2[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(st.s[i])));
+      const uint16_t two = *reinterpret_cast<const uint16_t*>(slot + 1024 + 128 * i + lane * 4 + (t & 1) * 2);
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
       s2[i][0] = __byte_perm(h2, h2, 0x1010);
       s2[i][1] = __byte_perm(h2, h2, 0x3232);
     }
-    const uint32_t c0[4] = {st.c[0].x, st.c[0].y, st.c[0].z, st.c[0].w};
-    const uint32_t c1[4] = {st.c[1].x, st.c[1].y, st.c[1].z, st.c[1].w};
+    const uint4 q0 = *reinterpret_cast<const uint4*>(slot + lane * 16);
+    const uint4 q1 = *reinterpret_cast<const uint4*>(slot + 512 + lane * 16);
+    const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w};
+    const uint32_t c1[4] = {q1.x, q1.y, q1.z, q1.w};
+    float one[NT][4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint32_t a0[4], a1[4];
+      e2m1x8_to_f16x2(c0[w], a0);
+      e2m1x8_to_f16x2(c1[w], a1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a0[j] = mul_f16x2(e2m1x2_to_f16x2((c0[w] >> (8 * j)) & 0xFFu), s2[0][w >> 1]);
-        a1[j] = mul_f16x2(e2m1x2_to_f16x2((c1[w] >> (8 * j)) & 0xFFu), s2[1][w >> 1]);
+        a0[j] = mul_f16x2(a0[j], s2[0][w >> 1]);
+        a1[j] = mul_f16x2(a1[j], s2[1][w >> 1]);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 xb = *reinterpret_cast<const uint4*>(xs + (8 * n + g) * pitch + grp * 256 + w * 64 + t * 16);
-        mma_16x8x16(acc[n], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
-        mma_16x8x16(acc[n], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+        const uint4 xb = *reinterpret_cast<const uint4*>(xlane[n] + step * 256 + w * 64);
+        if (w == 0) {
+          mma_16x8x16_from0(one[n], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+        } else {
+          mma_16x8x16(one[n], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+        }
+        mma_16x8x16(one[n], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] += one[n][i];
   };
-  // value i of lane's fragment: weight row g or g + 8 of the strip, row 2 t or 2 t + 1 of x
-  auto put = [&](int64_t strip, int n, int i, float v) {
+  // Value i of lane's fragment: weight row g or g + 8 of the strip, row 2 t or 2 t + 1 of x
+  float bias[2] = {0.0f, 0.0f};
+  auto load_bias = [&](int strip) {
+    const int64_t row = static_cast<int64_t>(strip >> 3) * 128 + (g >> 2) * 32 + (strip & 7) * 4 + (g & 3);
+    if (a.bias != nullptr) {
+      if (row < a.N) bias[0] = __ldg(a.bias + row);
+      if (row + 64 < a.N) bias[1] = __ldg(a.bias + row + 64);
+    }
+  };
+  auto put = [&](int strip, int n, int i, float v) {
     const int m = 8 * n + 2 * t + (i & 1);
-    const int64_t row = (strip >> 3) * 128 + (g >> 2) * 32 + (i >> 1) * 64 + (strip & 7) * 4 + (g & 3);
+    const int64_t row = static_cast<int64_t>(strip >> 3) * 128 + (g >> 2) * 32 + (i >> 1) * 64 + (strip & 7) * 4 + (g & 3);
     if (m >= tokens || row >= a.N) return;
-    if (a.bias != nullptr) v += a.bias[row];
+    v += bias[i >> 1];
     const int64_t at = (m0 + m) * a.ldd + row;
     if (a.out_kind == 2) {
       static_cast<float*>(a.D)[at] = v;
@@ -253,46 +374,51 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     }
   };
 
-  const int64_t per_iter = ncluster * rows_at_once;
-  const int64_t iters = (a.strips + per_iter - 1) / per_iter;
   int buf = 0, in_round = 0;
-  int64_t round_base = 0;  // first iteration of the round
-  for (int64_t it = 0; it < iters; ++it) {
-    const int64_t strip = it * per_iter + cid * rows_at_once + wr;
+  int it = 0, round_base = 0;  // strip iteration, first iteration of the round
+  // The end of a strip: its pieces of K are joined over the warps, and over the cluster.
+  auto finish = [&]() {
+    const int strip = it * a.strips_at_once + cid * rows_at_once + wr;
     const bool have = strip < a.strips;
+    float sum[4 * NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    if (have) {
-      const int64_t tile = strip >> 3;
-      const int r = static_cast<int>(strip & 7) * 4 + (g & 3);
-      const int64_t n0 = tile * 128 + (g >> 2) * 32 + r;
-      for (int grp = gb; grp < ge; ++grp) {
-        GemvStep st;
-        load_step(tile, r, n0, grp, st);
-        compute(grp, st);
-      }
+    for (int i = 0; i < 4 * NT; ++i) {
+      sum[i] = acc[i >> 2][i & 3];
+      acc[i >> 2][i & 3] = 0.0f;
     }
-    float* mine = red + ((buf * WARPS + warp) * 32 + lane) * 4 * NT;
+    bool mine = have;
+    if (kwarps > 1) {
+      float* slot = red + ((buf * WARPS + warp) * 32 + lane) * 4 * NT;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < NT; ++i)
+        *reinterpret_cast<float4*>(slot + 4 * i) = make_float4(sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
+      named_barrier(1 + wr, 32 * kwarps);
+      // the warps of a strip take turns at adding up its pieces
+      mine = have && wk == (it & (kwarps - 1));
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mine[4 * n + i] = acc[n][i];
-    __syncthreads();
-    // the warps of a strip take turns at adding up its pieces of K
-    if (wk == static_cast<int>(it) % a.kwarps && have) {
-      float sum[4 * NT];
+        for (int i = 0; i < 4 * NT; ++i) sum[i] = 0.0f;
+        for (int w = 0; w < kwarps; ++w) {
+          const float* p = red + ((buf * WARPS + wr * kwarps + w) * 32 + lane) * 4 * NT;
 #pragma unroll
-      for (int i = 0; i < 4 * NT; ++i) sum[i] = 0.0f;
-      for (int w = 0; w < a.kwarps; ++w) {
-        const float* p = red + ((buf * WARPS + wr * a.kwarps + w) * 32 + lane) * 4 * NT;
-#pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) sum[i] += p[i];
+          for (int i = 0; i < NT; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
+            sum[4 * i] += f.x;
+            sum[4 * i + 1] += f.y;
+            sum[4 * i + 2] += f.z;
+            sum[4 * i + 3] += f.w;
+          }
+        }
       }
+      buf ^= 1;
+    }
+    if (mine) {
 #pragma unroll
-      for (int i = 0; i < 4 * NT; ++i) sum[i] = sum[i] * G * inv[8 * (i >> 2) + 2 * t + (i & 1)];
-      if (a.cluster == 1) {
+      for (int i = 0; i < 4 * NT; ++i) {
+        const int m = 8 * (i >> 2) + 2 * t + (i & 1);
+        sum[i] = sum[i] * G * (m < tokens ? inv[m] : 0.0f);
+      }
+      if (cluster == 1) {
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i) put(strip, i >> 2, i & 3, sum[i]);
       } else {
@@ -301,33 +427,53 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
         for (int i = 0; i < 4 * NT; ++i) p[i] = sum[i];
       }
     }
-    buf ^= 1;
-    if (a.cluster > 1) {
+    if (cluster > 1) {
       in_round += rows_at_once;
-      if (in_round + rows_at_once > ROUND || it == iters - 1) {
+      if (in_round + rows_at_once > ROUND || it == a.iters - 1) {
         cluster_sync_all();  // every CTA's pieces of this round's strips are written
-        const int have_slots = in_round;
-        for (int s = rank + a.cluster * warp; s < have_slots; s += a.cluster * WARPS) {
-          const int64_t sit = round_base + s / rows_at_once;
-          const int64_t st = sit * per_iter + cid * rows_at_once + s % rows_at_once;
+        for (int s = rank + cluster * warp; s < in_round; s += cluster * WARPS) {
+          const int st = (round_base + s / rows_at_once) * a.strips_at_once + cid * rows_at_once + s % rows_at_once;
           if (st >= a.strips) continue;
+          load_bias(st);
           const uint32_t at = smem_u32(part + (s * 32 + lane) * 4 * NT);
-          float sum[4 * NT];
+          float all[4 * NT];
 #pragma unroll
-          for (int i = 0; i < 4 * NT; ++i) sum[i] = 0.0f;
-          for (int c = 0; c < a.cluster; ++c) {
+          for (int i = 0; i < 4 * NT; ++i) all[i] = 0.0f;
+#pragma unroll 4
+          for (int c = 0; c < cluster; ++c) {
             const uint32_t remote = mapa_shared(at, c);
 #pragma unroll
-            for (int i = 0; i < 4 * NT; ++i) sum[i] += ld_cluster_f32(remote + 4 * i);
+            for (int i = 0; i < NT; ++i) {
+              const float4 f = ld_cluster_f32x4(remote + 16 * i);
+              all[4 * i] += f.x;
+              all[4 * i + 1] += f.y;
+              all[4 * i + 2] += f.z;
+              all[4 * i + 3] += f.w;
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 4 * NT; ++i) put(st, i >> 2, i & 3, sum[i]);
+          for (int i = 0; i < 4 * NT; ++i) put(st, i >> 2, i & 3, all[i]);
         }
         cluster_sync_all();  // no CTA overwrites or leaves before the others have read
         in_round = 0;
         round_base = it + 1;
       }
     }
+    ++it;
+  };
+
+  const uint8_t* const ring_warp = ring + warp * (DEPTH * SLOT);
+  int slot = 0;
+  while (it < a.iters) {
+    const int strip = it * a.strips_at_once + cid * rows_at_once + wr;
+    if (cluster == 1 && wk == (it & (kwarps - 1)) && strip < a.strips) load_bias(strip);
+    for (int step = 0; step < a.per; ++step) {
+      copy_async_wait<DEPTH - 1>();
+      if (gb + step < groups) compute(step, ring_warp + slot * SLOT);
+      load(my_ring + slot * SLOT);
+      slot = (slot + 1) & (DEPTH - 1);
+    }
+    finish();
   }
 }
 

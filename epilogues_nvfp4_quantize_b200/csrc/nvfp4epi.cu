@@ -42,8 +42,10 @@ struct DeviceInfo {
   // false>, <Y = true>
   int quant_ctas_per_sm[4] = {0, 0, 0, 0};
   int mx_ctas_per_sm[2] = {0, 0};  // resident CTAs of mx_quantize_kernel<V8 = false, true>
-  // clusters of gemv_nvfp4_kernel<NT = 1, 2> that fit at once, by log2 of the cluster size
-  int gemv_clusters[2][4] = {};
+  // clusters of gemv_nvfp4_kernel that fit at once, by log2 of the cluster size (all instances take
+  // one CTA per SM)
+  int gemv_clusters[4] = {};
+  bool gemv_attr_set[2] = {};
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mutex;
@@ -840,73 +842,113 @@ namespace {
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int64_t out_size(int dtype) { return dtype == NVFP4_OUT_F32 ? 4 : 2; }
+// Launch with programmatic dependent launch: the kernels of this section let the next kernel start
+// launching at once and wait (griddepcontrol.wait) for the previous one before they touch memory, so
+// in a run of them the launch of each overlaps the end of the one before.
+template <class Args>
+nvfp4_status launch_dependent(void (*kern)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                              const Args& args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return NVFP4_ERR_CUDA;
+  }
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return NVFP4_OK;
+}
+
 bool is_dtype(int d) { return d == NVFP4_OUT_BF16 || d == NVFP4_OUT_F16 || d == NVFP4_OUT_F32; }
 
 template <int NT>
 nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t stream) {
   using namespace nvfp4::gemvcfg;
-  auto kern = nvfp4::gemv_nvfp4_kernel<NT>;
+  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 8>, nvfp4::gemv_nvfp4_kernel<NT, 4>};
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
   int clusters[4];
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (info->gemv_clusters[NT - 1][0] == 0) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM) != cudaSuccess)
-        return NVFP4_ERR_CUDA;
-      for (int i = 3; i >= 0; --i) {
+    if (!info->gemv_attr_set[NT - 1]) {
+      for (auto kern : kerns) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM) != cudaSuccess)
+          return NVFP4_ERR_CUDA;
+      }
+      cfg.numAttrs = 1;
+      cfg.dynamicSmemBytes = MAX_SMEM;
+      for (int i = 0; i < 4; ++i) {
         attr[0].val.clusterDim.x = 1u << i;
         cfg.gridDim = dim3(static_cast<unsigned>(info->sm_count >> i << i), 1, 1);
-        cfg.dynamicSmemBytes = MAX_SMEM;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return NVFP4_ERR_CUDA;
-        info->gemv_clusters[NT - 1][i] = n;
+        if (cudaOccupancyMaxActiveClusters(&n, kerns[0], &cfg) != cudaSuccess || n <= 0) return NVFP4_ERR_CUDA;
+        info->gemv_clusters[i] = n;
       }
+      info->gemv_attr_set[NT - 1] = true;
     }
-    std::memcpy(clusters, info->gemv_clusters[NT - 1], sizeof(clusters));
+    std::memcpy(clusters, info->gemv_clusters, sizeof(clusters));
   }
   // How K is cut: over the CTAs of a cluster (as far as x has to, to fit in shared memory, or to
   // occupy the SMs when the weight has few rows) and over the warps of a CTA. The cost of a choice
   // is the steps of its longest warp, plus about one step per join of warps and four per join of a
-  // cluster.
-  const int64_t groups = (a.K + GROUP - 1) / GROUP;
+  // cluster. Eight steps in flight where they fit beside x, else four.
+  const int groups = static_cast<int>((a.K + GROUP - 1) / GROUP);
   int64_t best = -1;
-  int best_i = 0;
+  int depth_i = 0;
   for (int i = 0; i < 4; ++i) {
-    const int64_t slice = (groups + (1 << i) - 1) >> i;  // groups per CTA
-    if (slice * GROUP > (1 << 20) || nvfp4::gemv_smem(NT, static_cast<int>(slice * GROUP), 1 << i) > MAX_SMEM) continue;
+    const int slice = (groups + (1 << i) - 1) >> i;  // groups per CTA
+    const int d = nvfp4::gemv_smem(NT, 8, a.M, slice * GROUP, 1 << i) <= MAX_SMEM ? 0 : 1;
+    if (d == 1 && nvfp4::gemv_smem(NT, 4, a.M, slice * GROUP, 1 << i) > MAX_SMEM) continue;
     if (i > 0 && slice * ((1 << i) - 1) >= groups) continue;  // a CTA without columns
-    for (int kw = 1; kw <= WARPS; kw <<= 1) {
-      const int64_t per_iter = static_cast<int64_t>(clusters[i]) * (WARPS / kw);
-      const int64_t iters = (a.strips + per_iter - 1) / per_iter;
-      const int64_t rounds = i == 0 ? 0 : (iters * (WARPS / kw) + ROUND - 1) / ROUND;
-      const int64_t cost = iters * ((slice + kw - 1) / kw + (kw > 1 ? 1 : 0)) + 4 * rounds;
+    for (int kw = 0; 1 << kw <= WARPS; ++kw) {
+      const int per_iter = clusters[i] * (WARPS >> kw);
+      const int iters = (a.strips + per_iter - 1) / per_iter;
+      const int per = (slice + (1 << kw) - 1) >> kw;
+      const int64_t rounds = i == 0 ? 0 : (static_cast<int64_t>(iters) * (WARPS >> kw) + ROUND - 1) / ROUND;
+      const int64_t cost = static_cast<int64_t>(iters) * (per + (kw > 0 ? 1 : 0)) + 4 * rounds;
       if (best < 0 || cost < best) {
         best = cost;
-        best_i = i;
-        a.kwarps = kw;
+        depth_i = d;
+        a.cluster_log2 = i;
+        a.kwarps_log2 = kw;
+        a.per = per;
+        a.iters = iters;
+        a.kslice = slice * GROUP;
       }
     }
   }
   if (best < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  a.cluster = 1 << best_i;
-  a.kslice = static_cast<int>(((groups + a.cluster - 1) >> best_i) * GROUP);
-  const int64_t per_cluster = WARPS / a.kwarps;
-  int64_t n = (a.strips + per_cluster - 1) / per_cluster;
-  if (n > clusters[best_i]) n = clusters[best_i];
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
-  cfg.gridDim = dim3(static_cast<unsigned>(n * a.cluster), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)), 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(nvfp4::gemv_smem(NT, a.kslice, a.cluster));
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+  const int per_cluster = WARPS >> a.kwarps_log2;
+  int n = (a.strips + per_cluster - 1) / per_cluster;
+  if (n > clusters[a.cluster_log2]) n = clusters[a.cluster_log2];
+  a.strips_at_once = n * per_cluster;
+  attr[0].val.clusterDim.x = 1u << a.cluster_log2;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(n << a.cluster_log2), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)), 1);
+  cfg.dynamicSmemBytes =
+      static_cast<size_t>(nvfp4::gemv_smem(NT, depth_i == 0 ? 8 : 4, a.M, a.kslice, 1 << a.cluster_log2));
+  if (cudaLaunchKernelEx(&cfg, kerns[depth_i], a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return NVFP4_ERR_CUDA;
+  }
   g_launches.fetch_add(1, std::memory_order_relaxed);
-  return launch_status();
+  return NVFP4_OK;
 }
 
 }  // namespace
@@ -943,8 +985,10 @@ NVFP4_API nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t
   a.D = D;
   a.ldd = ldd;
   a.out_kind = out_dtype;
-  a.strips = (B.rows + 127) / 128 * 8;
-  return M <= 8 ? launch_gemv<1>(info, a, stream) : launch_gemv<2>(info, a, stream);
+  a.strips = static_cast<int>((B.rows + 127) / 128 * 8);
+  // 16 rows at a time, or 8 where 16 rows of a very long K do not fit in a cluster's shared memory
+  st = M > 8 ? launch_gemv<2>(info, a, stream) : NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return st == NVFP4_ERR_UNSUPPORTED_SHAPE ? launch_gemv<1>(info, a, stream) : st;
 }
 
 namespace {
@@ -985,34 +1029,27 @@ nvfp4_status check_norm(const nvfp4_norm_inputs* in) {
 }
 
 template <class ST>
-void launch_norm(const nvfp4::NormArgs& a, int64_t rows, cudaStream_t stream) {
+nvfp4_status launch_norm(const nvfp4::NormArgs& a, int64_t rows, cudaStream_t stream) {
   const int64_t vecs = a.cols / 8;
   if (vecs <= 128) {  // a warp per row, four rows per CTA
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    if (vecs <= 32) {
-      nvfp4::residual_norm_kernel<ST, 1, true><<<grid, 128, 0, stream>>>(a);
-    } else if (vecs <= 64) {
-      nvfp4::residual_norm_kernel<ST, 2, true><<<grid, 128, 0, stream>>>(a);
-    } else {
-      nvfp4::residual_norm_kernel<ST, 4, true><<<grid, 128, 0, stream>>>(a);
-    }
-  } else {
-    const int threads = static_cast<int>((vecs + 63) / 64 * 32);
-    nvfp4::residual_norm_kernel<ST, 2, false><<<static_cast<unsigned>(rows), threads, 0, stream>>>(a);
+    auto kern = vecs <= 32   ? nvfp4::residual_norm_kernel<ST, 1, true>
+                : vecs <= 64 ? nvfp4::residual_norm_kernel<ST, 2, true>
+                             : nvfp4::residual_norm_kernel<ST, 4, true>;
+    return launch_dependent(kern, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, a);
   }
+  return launch_dependent(nvfp4::residual_norm_kernel<ST, 2, false>, dim3(static_cast<unsigned>(rows)),
+                          static_cast<int>((vecs + 63) / 64 * 32), 0, stream, a);
 }
 
 template <class ST>
-void launch_norm_grad(const nvfp4::NormGradArgs& a, cudaStream_t stream) {
+nvfp4_status launch_norm_grad(const nvfp4::NormGradArgs& a, cudaStream_t stream) {
   const int64_t vecs = a.cols / 8;
-  const unsigned grid = static_cast<unsigned>(a.chunks);
-  if (vecs <= 512) {
-    nvfp4::residual_norm_grad_kernel<ST, 1><<<grid, static_cast<int>((vecs + 31) / 32 * 32), 0, stream>>>(a);
-  } else if (vecs <= 1024) {
-    nvfp4::residual_norm_grad_kernel<ST, 2><<<grid, static_cast<int>((vecs + 63) / 64 * 32), 0, stream>>>(a);
-  } else {
-    nvfp4::residual_norm_grad_kernel<ST, 4><<<grid, static_cast<int>((vecs + 127) / 128 * 32), 0, stream>>>(a);
-  }
+  const int nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+  auto kern = nv == 1   ? nvfp4::residual_norm_grad_kernel<ST, 1>
+              : nv == 2 ? nvfp4::residual_norm_grad_kernel<ST, 2>
+                        : nvfp4::residual_norm_grad_kernel<ST, 4>;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)),
+                          static_cast<int>((vecs + 32 * nv - 1) / (32 * nv) * 32), 0, stream, a);
 }
 
 // Pieces that the rows are cut into for the gradient: two CTAs per SM of a B200 at 4096 columns, more
@@ -1079,13 +1116,8 @@ NVFP4_API nvfp4_status residual_norm(const nvfp4_norm_inputs* in, void* x_out, i
     a.q_gscale = hq->gscale;
   }
   a.stats = stats;
-  if (in->stream_dtype == NVFP4_OUT_F32) {
-    launch_norm<float>(a, rows, stream);
-  } else {
-    launch_norm<uint16_t>(a, rows, stream);
-  }
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return launch_status();
+  return in->stream_dtype == NVFP4_OUT_F32 ? launch_norm<float>(a, rows, stream)
+                                           : launch_norm<uint16_t>(a, rows, stream);
 }
 
 NVFP4_API int64_t residual_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t batches) {
@@ -1167,33 +1199,23 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
     a.seq_part = static_cast<float*>(workspace);
     if (weights) a.w_part = a.seq_part + (a.chunks + in->batches) * 3 * cols;
   }
-  if (in->stream_dtype == NVFP4_OUT_F32) {
-    launch_norm_grad<float>(a, stream);
-  } else {
-    launch_norm_grad<uint16_t>(a, stream);
-  }
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  if ((st = launch_status()) != NVFP4_OK || !(seq || weights)) return st;
+  st = in->stream_dtype == NVFP4_OUT_F32 ? launch_norm_grad<float>(a, stream) : launch_norm_grad<uint16_t>(a, stream);
+  if (st != NVFP4_OK || !(seq || weights)) return st;
   const int64_t by = !seq ? 0 : in->batches < 1024 ? in->batches : 1024;
   const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(by + 1));
-  nvfp4::norm_grad_reduce_kernel<<<grid, 256, 0, stream>>>(a);
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return launch_status();
+  return launch_dependent(nvfp4::norm_grad_reduce_kernel, grid, 256, 0, stream, a);
 }
 
 namespace {
 
 template <class T>
-void launch_rope(const nvfp4::RopeArgs& a, bool interleaved, size_t smem, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
-  constexpr int T0 = nvfp4::ropecfg::THREADS;
-  if (interleaved) {
-    nvfp4::rope_kernel<T, nvfp4::ROPE_INTERLEAVED><<<grid, T0, smem, stream>>>(a);
-  } else if (a.npairs % nvfp4::RopeVec<T>::V == 0) {
-    nvfp4::rope_kernel<T, nvfp4::ROPE_HALVES><<<grid, T0, smem, stream>>>(a);
-  } else {  // the second half does not start on 16 bytes
-    nvfp4::rope_kernel<T, nvfp4::ROPE_HALVES_SCALAR><<<grid, T0, smem, stream>>>(a);
-  }
+nvfp4_status launch_rope(const nvfp4::RopeArgs& a, bool interleaved, size_t smem, cudaStream_t stream) {
+  // halves: with a number of pairs that 16 bytes do not divide, the second half is not aligned
+  auto kern = interleaved                                  ? nvfp4::rope_kernel<T, nvfp4::ROPE_INTERLEAVED>
+              : a.npairs % nvfp4::RopeVec<T>::V == 0 ? nvfp4::rope_kernel<T, nvfp4::ROPE_HALVES>
+                                                           : nvfp4::rope_kernel<T, nvfp4::ROPE_HALVES_SCALAR>;
+  return launch_dependent(kern, dim3(static_cast<unsigned>((a.rows + a.rows_per_cta - 1) / a.rows_per_cta)),
+                          nvfp4::ropecfg::THREADS, smem, stream, a);
 }
 
 }  // namespace
@@ -1267,13 +1289,7 @@ NVFP4_API nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t
   a.rows_per_cta = static_cast<int>(r);
   const size_t smem = static_cast<size_t>(r * n) * sizeof(float2);
   const bool inter = interleaved != 0;
-  if (dtype == NVFP4_OUT_F32) {
-    launch_rope<float>(a, inter, smem, stream);
-  } else if (dtype == NVFP4_OUT_F16) {
-    launch_rope<__half>(a, inter, smem, stream);
-  } else {
-    launch_rope<__nv_bfloat16>(a, inter, smem, stream);
-  }
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return launch_status();
+  return dtype == NVFP4_OUT_F32   ? launch_rope<float>(a, inter, smem, stream)
+         : dtype == NVFP4_OUT_F16 ? launch_rope<__half>(a, inter, smem, stream)
+                                  : launch_rope<__nv_bfloat16>(a, inter, smem, stream);
 }

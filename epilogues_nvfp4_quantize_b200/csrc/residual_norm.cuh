@@ -13,6 +13,7 @@
 
 #include "ptx.cuh"
 #include "codec.cuh"
+#include "quantize.cuh"
 
 namespace nvfp4 {
 
@@ -160,6 +161,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 template <class ST, int NV, bool ONE_WARP>
 __global__ void __launch_bounds__(ONE_WARP ? 128 : 1024) residual_norm_kernel(const NormArgs a) {
   __shared__ float red[3][32];
+  griddep_launch_dependents();
+  griddep_wait();
   const int threads = ONE_WARP ? 32 : blockDim.x;
   const int t = ONE_WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t row = ONE_WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
@@ -398,6 +401,8 @@ __device__ __forceinline__ void cta_sum6(float (&s)[6], float* red) {
 template <class ST, int NV>
 __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormGradArgs a) {
   __shared__ float red[2][32 * 8];
+  griddep_launch_dependents();
+  griddep_wait();
   const int g = blockIdx.x;
   const int64_t r0 = norm_chunk_row(a.rows, a.chunks, g), r1 = norm_chunk_row(a.rows, a.chunks, g + 1);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
@@ -567,6 +572,8 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormGradA
 // Eight rows of threads share the slots and are joined in a fixed order.
 __global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArgs a) {
   __shared__ float red[3][8][33];
+  griddep_launch_dependents();
+  griddep_wait();
   const int cx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + cx;
   const bool live = col < a.cols;

@@ -13,6 +13,7 @@
 
 #include "ptx.cuh"
 #include "codec.cuh"
+#include "quantize.cuh"
 
 namespace nvfp4 {
 
@@ -128,6 +129,8 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   using RV = RopeVec<T>;
   constexpr int V = RV::V;
   extern __shared__ float2 rope_cs[];
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
   const int nrows = static_cast<int>(a.rows - row0 < a.rows_per_cta ? a.rows - row0 : a.rows_per_cta);
   rope_table(a, row0, nrows, rope_cs);
