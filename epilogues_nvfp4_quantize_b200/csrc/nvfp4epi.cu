@@ -46,6 +46,7 @@ struct DeviceInfo {
   // one CTA per SM)
   int gemv_clusters[4] = {};
   bool gemv_attr_set[2] = {};
+  bool norm_grad_attr_set[12] = {};  // residual_norm_grad_kernel, by stream type, NV and POST
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mutex;
@@ -1041,23 +1042,56 @@ nvfp4_status launch_norm(const nvfp4::NormArgs& a, int64_t rows, cudaStream_t st
                           static_cast<int>((vecs + 63) / 64 * 32), 0, stream, a);
 }
 
-template <class ST>
-nvfp4_status launch_norm_grad(const nvfp4::NormGradArgs& a, cudaStream_t stream) {
-  const int64_t vecs = a.cols / 8;
-  const int nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
-  auto kern = nv == 1   ? nvfp4::residual_norm_grad_kernel<ST, 1>
-              : nv == 2 ? nvfp4::residual_norm_grad_kernel<ST, 2>
-                        : nvfp4::residual_norm_grad_kernel<ST, 4>;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)),
-                          static_cast<int>((vecs + 32 * nv - 1) / (32 * nv) * 32), 0, stream, a);
+// Eight-column vectors per thread of the gradient kernel, its threads, and how many of its CTAs
+// share an SM (by registers).
+void norm_grad_shape(int64_t cols, int* nv, int* threads, int* per_sm) {
+  const int64_t vecs = cols / 8;
+  *nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+  *threads = static_cast<int>((vecs + 32 * *nv - 1) / (32 * *nv) * 32);
+  *per_sm = nvfp4::normcfg::GRAD_THREADS / *threads;
 }
 
-// Pieces that the rows are cut into for the gradient: two CTAs per SM of a B200 at 4096 columns, more
-// where a row keeps fewer threads busy.
+// Pieces that the rows are cut into for the gradient: one per CTA that fits on a B200's 148 SMs.
 int64_t norm_chunks(int64_t rows, int64_t cols) {
-  const int64_t more = cols >= 4096 ? 1 : cols >= 2048 ? 2 : cols >= 1024 ? 4 : 8;
-  const int64_t n = 296 * more;
+  int nv, threads, per_sm;
+  norm_grad_shape(cols, &nv, &threads, &per_sm);
+  const int64_t n = 148ll * per_sm;
   return rows < n ? rows : n;
+}
+
+template <class ST, int NV, bool POST>
+nvfp4_status launch_norm_grad(DeviceInfo* info, nvfp4::NormGradArgs a, cudaStream_t stream) {
+  using namespace nvfp4::normcfg;
+  auto kern = nvfp4::residual_norm_grad_kernel<ST, NV, POST>;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    bool& set = info->norm_grad_attr_set[(sizeof(ST) == 4) + 2 * (NV / 2) + 6 * POST];
+    if (!set) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GRAD_SMEM) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+      set = true;
+    }
+  }
+  int nv, threads, per_sm;
+  norm_grad_shape(a.cols, &nv, &threads, &per_sm);
+  const int64_t stage = nvfp4::norm_grad_stage(a.cols, sizeof(ST), a.dxo != nullptr, a.dh != nullptr, a.y != nullptr);
+  int64_t stages = (GRAD_SMEM / per_sm - GRAD_OTHER) / stage;  // one row of the largest size fits
+  const int64_t most = (a.rows + a.chunks - 1) / a.chunks;
+  if (stages > GRAD_MAX_STAGES) stages = GRAD_MAX_STAGES;
+  if (stages > most) stages = most;
+  if (stages < 1) stages = 1;
+  a.stages = static_cast<int>(stages);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)), threads, static_cast<size_t>(stages * stage),
+                          stream, a);
+}
+
+template <class ST, bool POST>
+nvfp4_status launch_norm_grad(DeviceInfo* info, const nvfp4::NormGradArgs& a, cudaStream_t stream) {
+  int nv, threads, per_sm;
+  norm_grad_shape(a.cols, &nv, &threads, &per_sm);
+  return nv == 1   ? launch_norm_grad<ST, 1, POST>(info, a, stream)
+         : nv == 2 ? launch_norm_grad<ST, 2, POST>(info, a, stream)
+                   : launch_norm_grad<ST, 4, POST>(info, a, stream);
 }
 
 }  // namespace
@@ -1199,7 +1233,10 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
     a.seq_part = static_cast<float*>(workspace);
     if (weights) a.w_part = a.seq_part + (a.chunks + in->batches) * 3 * cols;
   }
-  st = in->stream_dtype == NVFP4_OUT_F32 ? launch_norm_grad<float>(a, stream) : launch_norm_grad<uint16_t>(a, stream);
+  st = in->stream_dtype == NVFP4_OUT_F32
+           ? (in->post_norm ? launch_norm_grad<float, true>(info, a, stream) : launch_norm_grad<float, false>(info, a, stream))
+           : (in->post_norm ? launch_norm_grad<uint16_t, true>(info, a, stream)
+                            : launch_norm_grad<uint16_t, false>(info, a, stream));
   if (st != NVFP4_OK || !(seq || weights)) return st;
   const int64_t by = !seq ? 0 : in->batches < 1024 ? in->batches : 1024;
   const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(by + 1));

@@ -370,54 +370,147 @@ struct NormGradArgs {
   float* dw;              // cols, or null
   float* dw_post;
   int chunks;
+  int stages;             // row buffers of the ring
   float* seq_part;        // (chunks + batches) x 3 x cols, or null (no sums)
   float* w_part;          // chunks x 2 x cols, or null (neither dw nor dw_post)
 };
 
 __device__ __forceinline__ int64_t norm_chunk_row(int64_t rows, int chunks, int64_t g) { return rows * g / chunks; }
 
-// Sums of six values per thread over the CTA (blockDim.x a multiple of 32): every thread gets
-// all six. `red` holds 32 x 8 floats.
-__device__ __forceinline__ void cta_sum6(float (&s)[6], float* red) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int k = 0; k < 6; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-  }
-  if (lane == 0) {
-#pragma unroll
-    for (int k = 0; k < 6; ++k) red[warp * 8 + k] = s[k];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 6; ++k) {
-    s[k] = lane < warps ? red[lane * 8 + k] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-  }
+namespace normcfg {
+constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
+constexpr int GRAD_MAX_STAGES = 8;
+constexpr int GRAD_SMEM = 220 * 1024;    // per SM, for its CTAs' row buffers and GRAD_OTHER each
+constexpr int GRAD_OTHER = 3584;         // a CTA's static and reserved shared memory
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+}  // namespace normcfg
+
+// Bytes of one row's buffer: the stream, its gradient, the gradient of h, the branch, the statistics
+// (absent ones take no room).
+__host__ __device__ constexpr int64_t norm_grad_stage(int64_t cols, int elem, bool dxo, bool dh, bool y) {
+  return cols * (elem * (dxo + dh) + 2 * (dh + y)) + 16;
 }
 
-template <class ST, int NV>
-__global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormGradArgs a) {
+// Sums over the CTA of the first N of six values per thread (N = 2 or 6); every thread gets them.
+// Within a warp, each of the first log2 exchanges halves the values a lane keeps (9 shuffles for
+// six sums instead of 30); lane 4 k then holds sum k. `red` holds 32 x 8 floats.
+template <int N>
+__device__ __forceinline__ void cta_sums(float (&s)[6], float* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float v;
+  if constexpr (N == 6) {
+    float a4[4], a2[2];
+    const bool h16 = (lane & 16) != 0, h8 = (lane & 8) != 0, h4 = (lane & 4) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = s[k], hi = k < 2 ? s[k + 4] : 0.0f;
+      a4[k] = (h16 ? hi : lo) + __shfl_xor_sync(0xffffffffu, h16 ? lo : hi, 16);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      a2[k] = (h8 ? a4[k + 2] : a4[k]) + __shfl_xor_sync(0xffffffffu, h8 ? a4[k] : a4[k + 2], 8);
+    v = (h4 ? a2[1] : a2[0]) + __shfl_xor_sync(0xffffffffu, h4 ? a2[0] : a2[1], 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    if ((lane & 3) == 0) red[warp * 8 + (lane >> 2)] = v;
+  } else {
+    const bool h16 = (lane & 16) != 0;
+    v = (h16 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, h16 ? s[0] : s[1], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((lane & 15) == 0) red[warp * 8 + (lane >> 4)] = v;
+  }
+  __syncthreads();
+  v = 0.0f;
+  for (int w = lane >> 3; w < warps; w += 4) v += red[w * 8 + (lane & 7)];
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = __shfl_sync(0xffffffffu, v, k);
+}
+
+// A CTA walks the rows of its piece; thread t holds the eight columns at 8 t (and with NV > 1 those
+// at 8 (t + i threads)). Rows come through a ring of row buffers, filled by bulk copies (one per
+// tensor and row, issued by one thread `stages` rows ahead), so the loads of the coming rows are in
+// flight while a row is reduced. The one barrier of a row's reduction is also what frees its buffer:
+// every thread has read its values by then.
+// POST: the branch has its norm (six row sums, else two). With NV = 1 the sequence's constants per
+// column stay in registers, else they are read again for each row (from L1).
+template <class ST, int NV, bool POST>
+__global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kernel(const NormGradArgs a) {
+  using namespace normcfg;
+  extern __shared__ __align__(128) uint8_t norm_rows[];
   __shared__ float red[2][32 * 8];
+  __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES];
+  __shared__ int abort_flag;
   griddep_launch_dependents();
   griddep_wait();
   const int g = blockIdx.x;
   const int64_t r0 = norm_chunk_row(a.rows, a.chunks, g), r1 = norm_chunk_row(a.rows, a.chunks, g + 1);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
+  const bool has_dxo = a.dxo != nullptr, has_dh = a.dh != nullptr, has_y = a.y != nullptr;
+  // the parts of a row buffer
+  const uint32_t stream_bytes = static_cast<uint32_t>(a.cols * sizeof(ST)), half_bytes = static_cast<uint32_t>(a.cols * 2);
+  const uint32_t at_dxo = has_dh ? stream_bytes : 0u, at_dh = at_dxo + (has_dxo ? stream_bytes : 0u);
+  const uint32_t at_y = at_dh + (has_dh ? half_bytes : 0u), at_stats = at_y + (has_y ? half_bytes : 0u);
+  const uint32_t stage_bytes = at_stats + 16u;
+
+  auto fetch = [&](int64_t row, int stage) {  // one thread
+    uint8_t* to = norm_rows + stage * stage_bytes;
+    uint64_t* bar = &full[stage];
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    if (has_dh) {
+      bulk_load(to, static_cast<const ST*>(a.x) + row * a.ldx, stream_bytes, bar);
+      bulk_load(to + at_dh, a.dh + row * a.lddh, half_bytes, bar);
+    }
+    if (has_dxo) bulk_load(to + at_dxo, static_cast<const ST*>(a.dxo) + row * a.lddxo, stream_bytes, bar);
+    if (has_y) bulk_load(to + at_y, a.y + row * a.ldy, half_bytes, bar);
+    bulk_load(to + at_stats, a.stats + 4 * row, 16u, bar);
+  };
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
+    fence_mbarrier_init();
+    for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
+  }
+  __syncthreads();
+
   bool live[NV];
-  int64_t col[NV];
+  int col[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    col[i] = 8 * static_cast<int64_t>(threadIdx.x + i * blockDim.x);
+    col[i] = 8 * static_cast<int>(threadIdx.x + i * blockDim.x);
     live[i] = col[i] < a.cols;
   }
   float s_dh[NV][8], s_dhx[NV][8], s_ty[NV][8];  // sums over the current sequence's rows
-  float cw[NV][8], gt[NV][8];                     // w (1 + scale) and the gate, of the sequence
+  constexpr int NC = NV == 1 ? 1 : 0;
+  float c_w[NC + 1][8], c_g[NC + 1][8], c_a[NC + 1][8];  // w (1 + scale), the gate, gate w_post
   bool first_flush = true;
   int64_t b = -1, seq_end = r0;
 
+  // the sequence's constants of vector i
+  auto constants = [&](int i, float (&cw)[8], float (&gt)[8], float (&ag)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) cw[k] = gt[k] = 1.0f;
+    if (a.scale != nullptr) {
+      load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], cw);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) cw[k] += 1.0f;
+    }
+    if (a.w != nullptr) {
+      load8_f32(a.w + col[i], ag);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) cw[k] *= ag[k];
+    }
+    if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], gt);
+    if constexpr (POST) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ag[k] = 1.0f;
+      if (a.w_post != nullptr) load8_f32(a.w_post + col[i], ag);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ag[k] *= gt[k];
+    }
+  };
   auto flush = [&]() {
     if (a.seq_part == nullptr) return;  // no sums are asked for
 #pragma unroll
@@ -432,12 +525,14 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormGradA
       }
       if (a.w_part != nullptr) {
         float* q = a.w_part + static_cast<int64_t>(g) * 2 * a.cols + col[i];
-        float sc[8];
-        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], sc);
+        float one[8], gt[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) one[k] = 0.0f, gt[k] = 1.0f;
+        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], one);
+        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], gt);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float one = a.scale != nullptr ? 1.0f + sc[k] : 1.0f;
-          const float w0 = one * s_dhx[i][k], p0 = gt[i][k] * s_ty[i][k];
+          const float w0 = (1.0f + one[k]) * s_dhx[i][k], p0 = gt[k] * s_ty[i][k];
           q[k] = first_flush ? w0 : q[k] + w0;
           q[a.cols + k] = first_flush ? p0 : q[a.cols + k] + p0;
         }
@@ -446,112 +541,114 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormGradA
     first_flush = false;
   };
 
-  int parity = 0;
+  int stage = 0;
+  uint32_t phase = 0u;
   for (int64_t row = r0; row < r1; ++row) {
+    bool skip = false;
     if (row >= seq_end) {
       if (b >= 0) flush();
       b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
       if (b < 0) {  // rows without a sequence are left as they are
         seq_end = row + 1;
-        continue;
+        skip = true;
+      } else {
+        seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s_dh[i][k] = s_dhx[i][k] = s_ty[i][k] = 0.0f;
+          if constexpr (NV == 1) {
+            if (live[0]) constants(0, c_w[0], c_g[0], c_a[0]);
+          }
+        }
       }
-      seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
+    }
+    (void)mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 80);
+    const uint8_t* buf = norm_rows + stage * stage_bytes;
+    if (skip) {
+      __syncthreads();
+    } else {
+      const float4 st = *reinterpret_cast<const float4*>(buf + at_stats);
+      const float mean = st.x, rstd = st.y, rstd_y = POST ? st.z : 1.0f;
+      float xh[NV][8], d[NV][8], t[NV][8], yh[NV][8];
+      float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s_dh[i][k] = s_dhx[i][k] = s_ty[i][k] = 0.0f;
-          cw[i][k] = gt[i][k] = 1.0f;
-        }
+        for (int k = 0; k < 8; ++k) xh[i][k] = d[i][k] = t[i][k] = yh[i][k] = 0.0f;
         if (!live[i]) continue;
-        if (a.scale != nullptr) {
-          load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], cw[i]);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) cw[i][k] += 1.0f;
-        }
-        if (a.w != nullptr) {
-          float w[8];
-          load8_f32(a.w + col[i], w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) cw[i][k] *= w[k];
-        }
-        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], gt[i]);
-      }
-    }
-    const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * row);
-    const float mean = st.x, rstd = st.y, rstd_y = a.post ? st.z : 1.0f;
-    float xh[NV][8], d[NV][8], t[NV][8], yh[NV][8], ag[NV][8];
-    float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) xh[i][k] = d[i][k] = t[i][k] = yh[i][k] = ag[i][k] = 0.0f;
-      if (!live[i]) continue;
-      Stream8<ST> v;
-      if (a.dxo != nullptr) {
-        v.load(a.dxo, row * a.lddxo + col[i]);
-        v.get(t[i]);
-      }
-      if (a.y != nullptr) {
-        load8_bf16(a.y + row * a.ldy + col[i], yh[i]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) yh[i][k] *= rstd_y;
-      }
-      if (a.dh != nullptr) {
-        v.load(a.x, row * a.ldx + col[i]);
-        v.get(xh[i]);
-        load8_bf16(a.dh + row * a.lddh + col[i], d[i]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          xh[i][k] = (xh[i][k] - mean) * rstd;
-          s_dh[i][k] += d[i][k];
-          s_dhx[i][k] = fmaf(d[i][k], xh[i][k], s_dhx[i][k]);
-          d[i][k] *= cw[i][k];
-          s[0] += d[i][k];
-          s[1] = fmaf(d[i][k], xh[i][k], s[1]);
-        }
-      }
-      if (a.post) {
-        float wp[8];
-        if (a.w_post != nullptr) load8_f32(a.w_post + col[i], wp);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          ag[i][k] = a.w_post != nullptr ? gt[i][k] * wp[k] : gt[i][k];
-          const float ay = ag[i][k] * yh[i][k];
-          s[2] = fmaf(ay, t[i][k], s[2]);
-          s[3] = fmaf(ay, d[i][k], s[3]);
-          s[4] += ay;
-          s[5] = fmaf(ay, xh[i][k], s[5]);
-        }
-      }
-    }
-    cta_sum6(s, red[parity]);
-    parity ^= 1;
-    const float m1 = a.norm == NORM_LAYER ? s[0] * inv_n : 0.0f, m2 = s[1] * inv_n;
-    const float m3 = a.post ? (s[2] + rstd * (s[3] - m1 * s[4] - m2 * s[5])) * inv_n : 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!live[i]) continue;
-      float o[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (a.dh != nullptr) t[i][k] = fmaf(rstd, d[i][k] - m1 - xh[i][k] * m2, t[i][k]);
-        s_ty[i][k] = fmaf(t[i][k], yh[i][k], s_ty[i][k]);
-        o[k] = a.alpha * t[i][k];
-      }
-      if (a.dx != nullptr) {
+        if constexpr (NV > 1) constants(i, c_w[0], c_g[0], c_a[0]);
         Stream8<ST> v;
-        v.round(o);
-        v.store(a.dx, row * a.lddx + col[i]);
-      }
-      if (a.dy != nullptr) {
+        if (has_dxo) {
+          v.load(buf + at_dxo, col[i]);
+          v.get(t[i]);
+        }
+        if (has_y) {
+          load8_bf16(reinterpret_cast<const uint16_t*>(buf + at_y) + col[i], yh[i]);
+          if constexpr (POST) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          o[k] = a.post ? rstd_y * (ag[i][k] * t[i][k] - yh[i][k] * m3) : gt[i][k] * t[i][k];
-        Stream8<uint16_t> v;
-        v.round(o);
-        v.store(a.dy, row * a.lddy + col[i]);
+            for (int k = 0; k < 8; ++k) yh[i][k] *= rstd_y;
+          }
+        }
+        if (has_dh) {
+          v.load(buf, col[i]);
+          v.get(xh[i]);
+          load8_bf16(reinterpret_cast<const uint16_t*>(buf + at_dh) + col[i], d[i]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            xh[i][k] = (xh[i][k] - mean) * rstd;
+            s_dh[i][k] += d[i][k];
+            s_dhx[i][k] = fmaf(d[i][k], xh[i][k], s_dhx[i][k]);
+            d[i][k] *= c_w[0][k];
+            s[0] += d[i][k];
+            s[1] = fmaf(d[i][k], xh[i][k], s[1]);
+          }
+        }
+        if constexpr (POST) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float ay = c_a[0][k] * yh[i][k];
+            s[2] = fmaf(ay, t[i][k], s[2]);
+            s[3] = fmaf(ay, d[i][k], s[3]);
+            s[4] += ay;
+            s[5] = fmaf(ay, xh[i][k], s[5]);
+          }
+        }
       }
+      cta_sums<POST ? 6 : 2>(s, red[static_cast<int>(row - r0) & 1]);
+      const float m1 = a.norm == NORM_LAYER ? s[0] * inv_n : 0.0f, m2 = s[1] * inv_n;
+      const float m3 = POST ? (s[2] + rstd * (s[3] - m1 * s[4] - m2 * s[5])) * inv_n : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live[i]) continue;
+        if constexpr (NV > 1) constants(i, c_w[0], c_g[0], c_a[0]);
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (has_dh) t[i][k] = fmaf(rstd, d[i][k] - m1 - xh[i][k] * m2, t[i][k]);
+          s_ty[i][k] = fmaf(t[i][k], yh[i][k], s_ty[i][k]);
+          o[k] = a.alpha * t[i][k];
+        }
+        if (a.dx != nullptr) {
+          Stream8<ST> v;
+          v.round(o);
+          v.store(a.dx, row * a.lddx + col[i]);
+        }
+        if (a.dy != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            o[k] = POST ? rstd_y * (c_a[0][k] * t[i][k] - yh[i][k] * m3) : c_g[0][k] * t[i][k];
+          Stream8<uint16_t> v;
+          v.round(o);
+          v.store(a.dy, row * a.lddy + col[i]);
+        }
+      }
+    }
+    // every thread has passed this row's barrier, so its buffer takes the next row
+    if (threadIdx.x == 0 && row + a.stages < r1) fetch(row + a.stages, stage);
+    if (++stage == a.stages) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
   if (b >= 0) flush();
