@@ -48,19 +48,25 @@ struct NormArgs {
 
 enum NormKind { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
 
-// Sequence of a row, or -1 when it has none (rows before the first offset or behind the last).
-// The offsets come from the device and are not checked: whatever they hold, the answer is -1
-// or in [0, batches).
+// Sequence of a row, or -1 when it has none (rows before the first offset or behind the last). All
+// lanes of a warp ask for the same row: each step probes 32 offsets at once, so up to 31 sequences
+// take one load. The offsets come from the device and are not checked: whatever they hold, the
+// answer is -1 or in [0, batches).
 __device__ __forceinline__ int64_t norm_sequence(const int* offsets, int64_t batches, int64_t rows_per_batch,
                                                  int64_t row) {
-  if (offsets == nullptr) return row / rows_per_batch;
-  int64_t lo = 0, hi = batches + 1;  // number of offsets <= row
+  if (offsets == nullptr) {  // rows fit in 31 bits
+    return static_cast<uint32_t>(row) / static_cast<uint32_t>(rows_per_batch);
+  }
+  int64_t lo = 0, hi = batches + 1;  // the number of offsets <= row is in [lo, hi]
   while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(__ldg(offsets + mid)) <= row) {
-      lo = mid + 1;
+    const int64_t step = (hi - lo + 31) >> 5, at = lo + (threadIdx.x & 31) * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, at < hi && static_cast<int64_t>(__ldg(offsets + at)) <= row));
+    if (c == 0) {
+      hi = lo;
     } else {
-      hi = mid;
+      const int64_t end = lo + c * step;
+      lo += (c - 1) * step + 1;
+      hi = end < hi ? end : hi;
     }
   }
   return lo > batches ? -1 : lo - 1;
@@ -684,9 +690,11 @@ __global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArg
   if (blockIdx.y == gridDim.y - 1) {
     float s0 = 0.0f, s1 = 0.0f;
     if (live && a.w_part != nullptr) {
-      for (int g = ty; g < a.chunks; g += 8) {
-        s0 += a.w_part[static_cast<int64_t>(g) * 2 * a.cols + col];
-        s1 += a.w_part[(static_cast<int64_t>(g) * 2 + 1) * a.cols + col];
+      const float* p = a.w_part + static_cast<int64_t>(ty) * 2 * a.cols + col;
+#pragma unroll 4
+      for (int g = ty; g < a.chunks; g += 8, p += 16 * a.cols) {
+        s0 += p[0];
+        s1 += p[a.cols];
       }
     }
     join(0, s0);
@@ -705,16 +713,18 @@ __global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArg
     if (e > a.rows) e = a.rows;
     float v[3] = {0.0f, 0.0f, 0.0f};
     if (s < e) {
-      // pieces that hold rows of [s, e): the first one found from an estimate, then in order
-      int64_t g0 = s * a.chunks / a.rows;
-      while (g0 > 0 && norm_chunk_row(a.rows, a.chunks, g0) > s) --g0;
+      // pieces that hold rows of [s, e) (every piece has rows): from estimates
+      int g0 = static_cast<int>(s * a.chunks / a.rows), g1 = static_cast<int>((e - 1) * a.chunks / a.rows);
       while (norm_chunk_row(a.rows, a.chunks, g0 + 1) <= s) ++g0;
-      for (int64_t g = g0 + ty; g < a.chunks && norm_chunk_row(a.rows, a.chunks, g) < e; g += 8) {
-        if (norm_chunk_row(a.rows, a.chunks, g + 1) == norm_chunk_row(a.rows, a.chunks, g) || !live) continue;
-        const float* p = a.seq_part + (g + b) * 3 * a.cols + col;
-        v[0] += p[0];
-        v[1] += p[a.cols];
-        v[2] += p[2 * a.cols];
+      while (g1 + 1 < a.chunks && norm_chunk_row(a.rows, a.chunks, g1 + 1) < e) ++g1;
+      if (live) {
+        const float* p = a.seq_part + (g0 + ty + b) * 3 * a.cols + col;
+#pragma unroll 4
+        for (int g = g0 + ty; g <= g1; g += 8, p += 24 * a.cols) {
+          v[0] += p[0];
+          v[1] += p[a.cols];
+          v[2] += p[2 * a.cols];
+        }
       }
     }
 #pragma unroll
