@@ -1240,7 +1240,7 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
   if (st != NVFP4_OK || !(seq || weights)) return st;
   const int64_t by = !seq ? 0 : in->batches < 1024 ? in->batches : 1024;
   const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(by + 1));
-  return launch_dependent(nvfp4::norm_grad_reduce_kernel, grid, 256, 0, stream, a);
+  return launch_dependent(nvfp4::norm_grad_reduce_kernel, grid, 32 * nvfp4::normcfg::REDUCE_ROWS, 0, stream, a);
 }
 
 namespace {

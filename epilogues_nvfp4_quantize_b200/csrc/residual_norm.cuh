@@ -146,6 +146,12 @@ __device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
   s.get(v);
 }
 
+__device__ __forceinline__ void store8_f32(float* p, float (&v)[8]) {
+  Stream8<float> s;
+  s.round(v);
+  s.store(p, 0);
+}
+
 // Sum over the threads of a row: one warp (ONE_WARP), or all of the CTA's (red: 32 floats,
 // flipped between two halves by the caller so that one barrier per sum suffices).
 template <bool ONE_WARP>
@@ -386,6 +392,7 @@ __device__ __forceinline__ int64_t norm_chunk_row(int64_t rows, int chunks, int6
 namespace normcfg {
 constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
 constexpr int GRAD_MAX_STAGES = 8;
+constexpr int REDUCE_ROWS = 32;
 constexpr int GRAD_SMEM = 220 * 1024;    // per SM, for its CTAs' row buffers and GRAD_OTHER each
 constexpr int GRAD_OTHER = 3584;         // a CTA's static and reserved shared memory
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
@@ -523,25 +530,32 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
     for (int i = 0; i < NV; ++i) {
       if (!live[i]) continue;
       float* p = a.seq_part + (g + b) * 3 * a.cols + col[i];
-      const float* const src[3] = {s_dh[i], s_dhx[i], s_ty[i]};
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        *reinterpret_cast<float4*>(p + k * a.cols) = make_float4(src[k][0], src[k][1], src[k][2], src[k][3]);
-        *reinterpret_cast<float4*>(p + k * a.cols + 4) = make_float4(src[k][4], src[k][5], src[k][6], src[k][7]);
-      }
+      store8_f32(p, s_dh[i]);
+      store8_f32(p + a.cols, s_dhx[i]);
+      store8_f32(p + 2 * a.cols, s_ty[i]);
       if (a.w_part != nullptr) {
         float* q = a.w_part + static_cast<int64_t>(g) * 2 * a.cols + col[i];
-        float one[8], gt[8];
+        float w0[8], p0[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) one[k] = 0.0f, gt[k] = 1.0f;
-        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], one);
-        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], gt);
+        for (int k = 0; k < 8; ++k) w0[k] = 0.0f, p0[k] = 1.0f;
+        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], w0);
+        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], p0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float w0 = (1.0f + one[k]) * s_dhx[i][k], p0 = gt[k] * s_ty[i][k];
-          q[k] = first_flush ? w0 : q[k] + w0;
-          q[a.cols + k] = first_flush ? p0 : q[a.cols + k] + p0;
+          w0[k] = (1.0f + w0[k]) * s_dhx[i][k];
+          p0[k] *= s_ty[i][k];
         }
+        if (!first_flush) {
+          float o[8];
+          load8_f32(q, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w0[k] += o[k];
+          load8_f32(q + a.cols, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) p0[k] += o[k];
+        }
+        store8_f32(q, w0);
+        store8_f32(q + a.cols, p0);
       }
     }
     first_flush = false;
@@ -672,38 +686,41 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
 
 // Adds up the slots of each sequence and the pieces' weight sums. Block (x, y): columns 32 x and
 // on; y < gridDim.y - 1 takes the sequences y, y + gridDim.y - 1, ..., the last y the weights.
-// Eight rows of threads share the slots and are joined in a fixed order.
-__global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArgs a) {
-  __shared__ float red[3][8][33];
+// 32 warps share the slots, one column per lane, and are joined in a fixed order (warp c then adds
+// column c over the warps). With 148 to 2368 slots it is the latency of a thread's loads one after
+// another that counts: 8 warps with 4 loads in flight took 12 us for 296 slots of 2048 columns.
+__global__ void __launch_bounds__(32 * normcfg::REDUCE_ROWS) norm_grad_reduce_kernel(const NormGradArgs a) {
+  using normcfg::REDUCE_ROWS;
+  __shared__ float red[3][REDUCE_ROWS][33];
   griddep_launch_dependents();
   griddep_wait();
-  const int cx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + cx;
-  const bool live = col < a.cols;
-  auto join = [&](int k, float v) { red[k][ty][cx] = v; };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;        // while adding slots
+  const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + warp;        // while joining
+  const bool live = col < a.cols, last = lane == 0 && out < a.cols;
   auto total = [&](int k) {
-    float v = 0.0f;
+    float v = red[k][lane][warp];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += red[k][i][cx];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
   if (blockIdx.y == gridDim.y - 1) {
     float s0 = 0.0f, s1 = 0.0f;
     if (live && a.w_part != nullptr) {
-      const float* p = a.w_part + static_cast<int64_t>(ty) * 2 * a.cols + col;
-#pragma unroll 4
-      for (int g = ty; g < a.chunks; g += 8, p += 16 * a.cols) {
+      const float* p = a.w_part + static_cast<int64_t>(warp) * 2 * a.cols + col;
+#pragma unroll 10
+      for (int g = warp; g < a.chunks; g += REDUCE_ROWS, p += 2 * REDUCE_ROWS * a.cols) {
         s0 += p[0];
         s1 += p[a.cols];
       }
     }
-    join(0, s0);
-    join(1, s1);
+    red[0][warp][lane] = s0;
+    red[1][warp][lane] = s1;
     __syncthreads();
-    if (ty == 0 && live) {
-      if (a.dw != nullptr) a.dw[col] = total(0);
-      if (a.dw_post != nullptr) a.dw_post[col] = total(1);
-    }
+    s0 = total(0);
+    s1 = total(1);
+    if (last && a.dw != nullptr) a.dw[out] = s0;
+    if (last && a.dw_post != nullptr) a.dw_post[out] = s1;
     return;
   }
   for (int64_t b = blockIdx.y; b < a.batches; b += gridDim.y - 1) {
@@ -718,9 +735,9 @@ __global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArg
       while (norm_chunk_row(a.rows, a.chunks, g0 + 1) <= s) ++g0;
       while (g1 + 1 < a.chunks && norm_chunk_row(a.rows, a.chunks, g1 + 1) < e) ++g1;
       if (live) {
-        const float* p = a.seq_part + (g0 + ty + b) * 3 * a.cols + col;
-#pragma unroll 4
-        for (int g = g0 + ty; g <= g1; g += 8, p += 24 * a.cols) {
+        const float* p = a.seq_part + (g0 + warp + b) * 3 * a.cols + col;
+#pragma unroll 5
+        for (int g = g0 + warp; g <= g1; g += REDUCE_ROWS, p += 3 * REDUCE_ROWS * a.cols) {
           v[0] += p[0];
           v[1] += p[a.cols];
           v[2] += p[2 * a.cols];
@@ -728,15 +745,15 @@ __global__ void __launch_bounds__(256) norm_grad_reduce_kernel(const NormGradArg
       }
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) join(k, v[k]);
+    for (int k = 0; k < 3; ++k) red[k][warp][lane] = v[k];
     __syncthreads();
-    if (ty == 0 && live) {
-      if (a.dshift != nullptr) a.dshift[b * a.lddshift + col] = total(0);
-      if (a.dscale != nullptr) a.dscale[b * a.lddscale + col] = a.w != nullptr ? total(1) * a.w[col] : total(1);
-      if (a.dgate != nullptr) {
-        const float v2 = total(2);
-        a.dgate[b * a.lddgate + col] = a.post && a.w_post != nullptr ? v2 * a.w_post[col] : v2;
-      }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = total(k);
+    if (last) {
+      if (a.dshift != nullptr) a.dshift[b * a.lddshift + out] = v[0];
+      if (a.dscale != nullptr) a.dscale[b * a.lddscale + out] = v[1] * (a.w != nullptr ? a.w[out] : 1.0f);
+      if (a.dgate != nullptr)
+        a.dgate[b * a.lddgate + out] = v[2] * (a.post && a.w_post != nullptr ? a.w_post[out] : 1.0f);
     }
     __syncthreads();
   }
