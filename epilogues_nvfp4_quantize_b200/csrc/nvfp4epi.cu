@@ -46,6 +46,7 @@ struct DeviceInfo {
   // one CTA per SM)
   int gemv_clusters[4] = {};
   bool gemv_attr_set[2] = {};
+  bool norm_attr_set[8] = {};        // residual_norm_ring_kernel, by stream type, NV and POST
   bool norm_grad_attr_set[12] = {};  // residual_norm_grad_kernel, by stream type, NV and POST
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -1029,9 +1030,52 @@ nvfp4_status check_norm(const nvfp4_norm_inputs* in) {
   return NVFP4_OK;
 }
 
+template <class ST, int NV, bool POST>
+nvfp4_status launch_norm_ring(DeviceInfo* info, const nvfp4::NormArgs& a, int threads, size_t smem, cudaStream_t stream) {
+  auto kern = nvfp4::residual_norm_ring_kernel<ST, NV, POST>;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    bool& set = info->norm_attr_set[(sizeof(ST) == 4) + 2 * (NV == 4) + 4 * POST];
+    if (!set) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, nvfp4::normcfg::SMEM) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+      set = true;
+    }
+  }
+  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)), threads, smem, stream, a);
+}
+
+// `rows`: with the rows that pad an NVFP4 output's block scales.
 template <class ST>
-nvfp4_status launch_norm(const nvfp4::NormArgs& a, int64_t rows, cudaStream_t stream) {
+nvfp4_status launch_norm(DeviceInfo* info, nvfp4::NormArgs a, int64_t rows, cudaStream_t stream) {
+  using namespace nvfp4::normcfg;
   const int64_t vecs = a.cols / 8;
+  // the ring kernel: CTAs that share an SM, and pieces of rows for all of them
+  const int nv = vecs <= 1024 ? 2 : 4;
+  const int threads = static_cast<int>((vecs + 32 * nv - 1) / (32 * nv) * 32);
+  int per_sm = FWD_THREADS / threads;
+  if (per_sm > 16) per_sm = 16;
+  const int64_t chunks = static_cast<int64_t>(info->sm_count) * per_sm;
+  if (a.rows >= RING_ROWS * chunks) {
+    const int64_t stage = nvfp4::norm_stage(a.cols, sizeof(ST), a.y != nullptr);
+    const int64_t vectors =
+        nv == 2 ? nvfp4::norm_vector_bytes(a.cols, a.mod_f32,
+                                           (a.gate != nullptr) + (a.scale != nullptr) + (a.shift != nullptr),
+                                           (a.w_post != nullptr) + (a.w != nullptr))
+                : 0;
+    int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // the largest size leaves room for one
+    if (stages > FWD_MAX_STAGES) stages = FWD_MAX_STAGES;
+    if (stages < 1) stages = 1;
+    a.chunks = static_cast<int>(chunks);
+    a.stages = static_cast<int>(stages);
+    const size_t smem = static_cast<size_t>(stages * stage + vectors);
+    if (nv == 2) {
+      return a.post ? launch_norm_ring<ST, 2, true>(info, a, threads, smem, stream)
+                    : launch_norm_ring<ST, 2, false>(info, a, threads, smem, stream);
+    }
+    return a.post ? launch_norm_ring<ST, 4, true>(info, a, threads, smem, stream)
+                  : launch_norm_ring<ST, 4, false>(info, a, threads, smem, stream);
+  }
   if (vecs <= 128) {  // a warp per row, four rows per CTA
     auto kern = vecs <= 32   ? nvfp4::residual_norm_kernel<ST, 1, true>
                 : vecs <= 64 ? nvfp4::residual_norm_kernel<ST, 2, true>
@@ -1067,7 +1111,7 @@ nvfp4_status launch_norm_grad(DeviceInfo* info, nvfp4::NormGradArgs a, cudaStrea
     std::lock_guard<std::mutex> lock(g_mutex);
     bool& set = info->norm_grad_attr_set[(sizeof(ST) == 4) + 2 * (NV / 2) + 6 * POST];
     if (!set) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GRAD_SMEM) != cudaSuccess)
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
         return NVFP4_ERR_CUDA;
       set = true;
     }
@@ -1075,14 +1119,18 @@ nvfp4_status launch_norm_grad(DeviceInfo* info, nvfp4::NormGradArgs a, cudaStrea
   int nv, threads, per_sm;
   norm_grad_shape(a.cols, &nv, &threads, &per_sm);
   const int64_t stage = nvfp4::norm_grad_stage(a.cols, sizeof(ST), a.dxo != nullptr, a.dh != nullptr, a.y != nullptr);
-  int64_t stages = (GRAD_SMEM / per_sm - GRAD_OTHER) / stage;  // one row of the largest size fits
+  const int64_t vectors =
+      nv == 1 ? nvfp4::norm_vector_bytes(a.cols, a.mod_f32, (a.gate != nullptr) + (a.scale != nullptr),
+                                         (a.w_post != nullptr) + (a.w != nullptr))
+              : 0;
+  int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // the largest size leaves room for one
   const int64_t most = (a.rows + a.chunks - 1) / a.chunks;
   if (stages > GRAD_MAX_STAGES) stages = GRAD_MAX_STAGES;
   if (stages > most) stages = most;
   if (stages < 1) stages = 1;
   a.stages = static_cast<int>(stages);
-  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)), threads, static_cast<size_t>(stages * stage),
-                          stream, a);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)), threads,
+                          static_cast<size_t>(stages * stage + vectors), stream, a);
 }
 
 template <class ST, bool POST>
@@ -1150,14 +1198,15 @@ NVFP4_API nvfp4_status residual_norm(const nvfp4_norm_inputs* in, void* x_out, i
     a.q_gscale = hq->gscale;
   }
   a.stats = stats;
-  return in->stream_dtype == NVFP4_OUT_F32 ? launch_norm<float>(a, rows, stream)
-                                           : launch_norm<uint16_t>(a, rows, stream);
+  return in->stream_dtype == NVFP4_OUT_F32 ? launch_norm<float>(info, a, rows, stream)
+                                           : launch_norm<uint16_t>(info, a, rows, stream);
 }
 
 NVFP4_API int64_t residual_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t batches) {
   if (rows <= 0 || cols <= 0 || batches <= 0) return -1;
   const int64_t n = norm_chunks(rows, cols);
-  return ((n + batches) * 3 + n * 2) * cols * static_cast<int64_t>(sizeof(float));
+  return ((n + batches) * 3 + n * 2) * cols * static_cast<int64_t>(sizeof(float)) +
+         2 * batches * static_cast<int64_t>(sizeof(int));
 }
 
 NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const float* stats,
@@ -1231,7 +1280,9 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
   a.chunks = static_cast<int>(norm_chunks(in->rows, cols));
   if (seq || weights) {
     a.seq_part = static_cast<float*>(workspace);
-    if (weights) a.w_part = a.seq_part + (a.chunks + in->batches) * 3 * cols;
+    float* const w_part = a.seq_part + (a.chunks + in->batches) * 3 * cols;
+    if (weights) a.w_part = w_part;
+    a.seq_pieces = reinterpret_cast<int*>(w_part + static_cast<int64_t>(a.chunks) * 2 * cols);
   }
   st = in->stream_dtype == NVFP4_OUT_F32
            ? (in->post_norm ? launch_norm_grad<float, true>(info, a, stream) : launch_norm_grad<float, false>(info, a, stream))

@@ -44,6 +44,7 @@ struct NormArgs {
   uint8_t* q_sf;
   const float* q_gscale;
   float* stats;           // rows x 4: mean, rstd, rstd of the branch, 0; or null
+  int chunks, stages;     // ring kernel: pieces of the rows, row buffers
 };
 
 enum NormKind { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
@@ -168,7 +169,28 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// One row per CTA (ONE_WARP: per warp); thread t holds the eight columns at 8 t, and with NV > 1
+// NVFP4 codes and scale of the eight bf16 values v at column col of a row. A block of 16 is two
+// lanes, a scale word (64 columns) eight: cols % 64 == 0, so each group of eight lanes is live as a
+// whole. All lanes of the warp call it.
+__device__ __forceinline__ void norm_quantize8(const NormArgs& a, const float (&v)[8], bool live, int64_t row,
+                                               int64_t col, int64_t nkb, float G, float enc) {
+  const int lane = threadIdx.x & 31;
+  float amax = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) amax = fmaxf(amax, live ? fabsf(v[k]) : 0.0f);
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  const uint32_t s = block_scale_code(amax, enc);
+  const float r = block_inv_scale(s, G);
+  uint32_t word = (lane & 1) ? 0u : s << (4 * (lane & 7));
+  word |= __shfl_xor_sync(0xffffffffu, word, 2);
+  word |= __shfl_xor_sync(0xffffffffu, word, 4);
+  if (live) {
+    *reinterpret_cast<uint32_t*>(a.q_codes + row * (a.cols >> 1) + (col >> 1)) = r > 0.0f ? block_codes8(v, r) : 0u;
+    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.q_sf + sf_word_offset(row, col >> 4, nkb)) = word;
+  }
+}
+
+// For few rows. One row per CTA (ONE_WARP: per warp); thread t holds the eight columns at 8 t, and with NV > 1
 // those at 8 (t + i threads).
 template <class ST, int NV, bool ONE_WARP>
 __global__ void __launch_bounds__(ONE_WARP ? 128 : 1024) residual_norm_kernel(const NormArgs a) {
@@ -311,24 +333,333 @@ __global__ void __launch_bounds__(ONE_WARP ? 128 : 1024) residual_norm_kernel(co
       out.round(v[i]);
       if (a.h != nullptr) out.store(a.h, row * a.ldh + col[i]);
     }
-    if (a.q_codes != nullptr) {
-      // a block of 16 is two lanes, a scale word (64 columns) eight: cols % 64 == 0, so each
-      // group of eight lanes is live as a whole
-      float amax = 0.0f;
+    if (a.q_codes != nullptr) norm_quantize8(a, v[i], live[i], row, col[i], nkb, G, enc);
+  }
+}
+
+namespace normcfg {
+constexpr int FWD_THREADS = 512;         // threads per SM that the ring kernel's registers allow
+constexpr int FWD_MAX_STAGES = 8;
+constexpr int RING_ROWS = 2;             // rows per CTA from which the ring kernel is taken
+constexpr int SMEM = 220 * 1024;         // per SM, for its CTAs' row buffers and SMEM_OTHER each
+constexpr int SMEM_OTHER = 3584;         // a CTA's static and reserved shared memory
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+}  // namespace normcfg
+
+// A sequence's vectors on their way to a CTA's registers: one bulk copy each into shared memory, all in
+// flight together. (Loaded straight into registers, each was waited for before the next was asked for,
+// and since all CTAs ask for the same lines at the start, that took 8 us of 4096 x 4096's 32.)
+struct NormVectors {
+  enum { GATE, SCALE, SHIFT, W_POST, W, COUNT };
+  uint32_t at[COUNT + 1];  // places in the buffer; absent ones take no room
+  __device__ __forceinline__ NormVectors(const void* gate, const void* scale, const void* shift, const void* w_post,
+                                         const void* w, int64_t cols, int mod_f32) {
+    const void* const p[COUNT] = {gate, scale, shift, w_post, w};
+    at[0] = 0u;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, live[i] ? fabsf(v[i][k]) : 0.0f);
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      const uint32_t s = block_scale_code(amax, enc);
-      const float r = block_inv_scale(s, G);
-      const int lane = threadIdx.x & 31;
-      uint32_t word = (lane & 1) ? 0u : s << (4 * (lane & 7));
-      word |= __shfl_xor_sync(0xffffffffu, word, 2);
-      word |= __shfl_xor_sync(0xffffffffu, word, 4);
-      if (live[i]) {
-        const uint32_t codes = r > 0.0f ? block_codes8(v[i], r) : 0u;
-        *reinterpret_cast<uint32_t*>(a.q_codes + row * (a.cols >> 1) + (col[i] >> 1)) = codes;
-        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.q_sf + sf_word_offset(row, col[i] >> 4, nkb)) = word;
+    for (int i = 0; i < COUNT; ++i)
+      at[i + 1] = at[i] + (p[i] == nullptr ? 0u : static_cast<uint32_t>(cols * (i >= W_POST || mod_f32 ? 4 : 2)));
+  }
+  __device__ __forceinline__ uint32_t bytes() const { return at[COUNT]; }
+  __device__ __forceinline__ void fetch(int i, uint8_t* buf, const void* p, int64_t first, int mod_f32,
+                                        uint64_t* bar) const {  // one thread
+    if (at[i + 1] == at[i]) return;
+    bulk_load(buf + at[i], static_cast<const char*>(p) + first * (i >= W_POST || mod_f32 ? 4 : 2), at[i + 1] - at[i], bar);
+  }
+  // Eight values of vector i, or eight times `none`.
+  __device__ __forceinline__ void get(int i, const uint8_t* buf, int col, int mod_f32, float none, float (&v)[8]) const {
+    if (at[i + 1] == at[i]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = none;
+    } else {
+      load8_mod(buf + at[i], i >= W_POST || mod_f32, col, v);
+    }
+  }
+};
+// Bytes of that buffer.
+__host__ __device__ constexpr int64_t norm_vector_bytes(int64_t cols, int mod_f32, int mods, int weights) {
+  return cols * (mods * (mod_f32 ? 4 : 2) + weights * 4);
+}
+
+__host__ __device__ constexpr int64_t norm_stage(int64_t cols, int elem, bool y) { return cols * (elem + 2 * y); }
+__device__ __forceinline__ int64_t norm_chunk_row(int64_t rows, int chunks, int64_t g) { return rows * g / chunks; }
+
+// residual_norm over many rows: a CTA walks a contiguous piece of them. Rows come through a ring of
+// row buffers, filled by bulk copies (one per tensor and row, issued by one thread `stages` rows
+// ahead), so coming rows are in flight while a row is reduced. A row's first barrier also frees its
+// buffer: every thread has read its values by then. Thread t holds the eight columns at 8 (t + i
+// threads), i < NV; with NV = 2 the sequence's modulation stays in registers, else it is read again for
+// each row (from L1).
+// What a row costs beside its elements (barriers, shuffles, the ring) is per warp, so fewer threads
+// with more columns each are faster: 4096 x 4096 with NV = 1 and 512 threads took 33.5 us, 7 of them for
+// the reductions.
+template <class ST, int NV, bool POST>
+__global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormArgs a) {
+  using namespace normcfg;
+  extern __shared__ __align__(128) uint8_t norm_rows[];
+  __shared__ float red[2][3][16];
+  __shared__ __align__(8) uint64_t full[FWD_MAX_STAGES], vec_full;
+  __shared__ int abort_flag;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t r0 = norm_chunk_row(a.rows, a.chunks, blockIdx.x), r1 = norm_chunk_row(a.rows, a.chunks, blockIdx.x + 1);
+  const bool has_y = a.y != nullptr;
+  const uint32_t x_bytes = static_cast<uint32_t>(a.cols * sizeof(ST)), y_bytes = has_y ? static_cast<uint32_t>(a.cols * 2) : 0u;
+  const uint32_t stage_bytes = x_bytes + y_bytes;
+  auto fetch = [&](int64_t row, int stage) {  // one thread
+    uint8_t* to = norm_rows + stage * stage_bytes;
+    mbar_arrive_expect_tx(&full[stage], stage_bytes);
+    bulk_load(to, static_cast<const ST*>(a.x) + row * a.ldx, x_bytes, &full[stage]);
+    if (has_y) bulk_load(to + x_bytes, a.y + row * a.ldy, y_bytes, &full[stage]);
+  };
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
+    mbar_init(&vec_full, 1);
+    fence_mbarrier_init();
+    for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
+  }
+  const int64_t nkb = a.cols >> 4;
+  if (a.q_codes != nullptr && blockIdx.x == gridDim.x - 1) {  // block scales of the rows that pad to 128 are 0
+    const int64_t words = (((a.rows + 127) & ~int64_t(127)) - a.rows) * (a.cols >> 6);
+    for (int64_t i = threadIdx.x; i < words; i += blockDim.x)
+      *reinterpret_cast<uint32_t*>(a.q_sf + sf_word_offset(a.rows + i / (a.cols >> 6), 4 * (i % (a.cols >> 6)), nkb)) = 0u;
+  }
+  __syncthreads();
+
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  bool live[NV];
+  int col[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    col[i] = 8 * static_cast<int>(threadIdx.x + i * blockDim.x);
+    live[i] = col[i] < a.cols;
+  }
+  float G = 0.0f, enc = 0.0f;
+  if (a.q_codes != nullptr) {
+    G = *a.q_gscale;
+    enc = scale_encode_factor(G);
+  }
+  constexpr int NC = NV == 2 ? NV : 1;
+  float cg[NC][8], cs[NC][8], ch[NC][8];  // gate w_post, w (1 + scale), shift
+  int64_t b = -1, seq_end = r0;
+  const int lane16 = threadIdx.x & 15, warps = blockDim.x >> 5;
+  auto warp_columns = [&](int w) {  // columns that warp w holds
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int left = static_cast<int>(a.cols) - 8 * (32 * w + i * static_cast<int>(blockDim.x));
+      n += left < 0 ? 0 : left < 256 ? left : 256;
+    }
+    return w < warps ? static_cast<float>(n) : 0.0f;
+  };
+  const float my_columns = warp_columns(threadIdx.x >> 5), its_columns = warp_columns(lane16);
+  const float my_inv = my_columns > 0.0f ? 1.0f / my_columns : 0.0f;
+  auto join = [&](float v) {  // sum over the lanes of a half-warp
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  // Sum over the CTA (at most 16 warps), one barrier.
+  auto cta_sum = [&](float v, float* rd) {
+    v = row_sum<true>(v, nullptr);
+    if ((threadIdx.x & 31) == 0) rd[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return join(lane16 < warps ? rd[lane16] : 0.0f);
+  };
+  // gate w_post, w (1 + scale) and shift of vector i, from the buffer (NV = 2) or from global memory
+  uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
+  const NormVectors vecs(a.gate, a.scale, a.shift, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
+  auto times = [](float (&v)[8], const float (&w)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= w[k];
+  };
+  auto plus1 = [](float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += 1.0f;
+  };
+  auto from_buffer = [&](int i, float (&c_g)[8], float (&c_s)[8], float (&c_h)[8]) {
+    float w[8];
+    vecs.get(NormVectors::GATE, vec_buf, col[i], a.mod_f32, 1.0f, c_g);
+    vecs.get(NormVectors::W_POST, vec_buf, col[i], a.mod_f32, 1.0f, w);
+    times(c_g, w);
+    vecs.get(NormVectors::SCALE, vec_buf, col[i], a.mod_f32, 0.0f, c_s);
+    plus1(c_s);
+    vecs.get(NormVectors::W, vec_buf, col[i], a.mod_f32, 1.0f, w);
+    times(c_s, w);
+    vecs.get(NormVectors::SHIFT, vec_buf, col[i], a.mod_f32, 0.0f, c_h);
+  };
+  auto constants_gate = [&](int i, float (&c_g)[8]) {
+    float w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c_g[k] = 1.0f;
+    if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], c_g);
+    if (POST && a.w_post != nullptr) {
+      load8_f32(a.w_post + col[i], w);
+      times(c_g, w);
+    }
+  };
+  auto constants_norm = [&](int i, float (&c_s)[8], float (&c_h)[8]) {
+    float w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c_s[k] = c_h[k] = 0.0f;
+    if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], c_s);
+    plus1(c_s);
+    if (a.w != nullptr) {
+      load8_f32(a.w + col[i], w);
+      times(c_s, w);
+    }
+    if (a.shift != nullptr) load8_mod(a.shift, a.mod_f32, b * a.ldshift + col[i], c_h);
+  };
+
+  int stage = 0;
+  uint32_t phase = 0u, vec_phase = 0u;
+  for (int64_t row = r0; row < r1; ++row) {
+    if (row >= seq_end) {
+      b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
+      if (b < 0) {  // rows without a sequence are left as they are
+        seq_end = row + 1;
+      } else {
+        seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
+        if constexpr (NC == NV) {
+          // a barrier lies behind since the last sequence's were read
+          if (threadIdx.x == 0) {
+            mbar_arrive_expect_tx(&vec_full, vecs.bytes());
+            vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::SHIFT, vec_buf, a.shift, b * a.ldshift, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
+          }
+          (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 82);
+          vec_phase ^= 1u;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (live[i]) from_buffer(i, cg[i], cs[i], ch[i]);
+          }
+        }
       }
+    }
+    (void)mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 81);
+    const uint8_t* buf = norm_rows + stage * stage_bytes;
+    bool freed = false;  // a barrier has been passed since the row's values were read
+    auto refill = [&]() {
+      if (!freed && threadIdx.x == 0 && row + a.stages < r1) fetch(row + a.stages, stage);
+      freed = true;
+    };
+    if (b >= 0) {
+      float (*rd)[16] = red[static_cast<int>(row - r0) & 1];
+      float v[NV][8];
+      Stream8<uint16_t> ys[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live[i]) continue;
+        Stream8<ST> xs;
+        xs.load(buf, col[i]);
+        xs.get(v[i]);
+        if (has_y) ys[i].load(buf + x_bytes, col[i]);
+      }
+      float rstd_y = 1.0f;
+      if constexpr (POST) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (!live[i]) continue;
+          float yv[8];
+          ys[i].get(yv);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) ss = fmaf(yv[k], yv[k], ss);
+        }
+        rstd_y = rsqrtf(cta_sum(ss, rd[0]) * inv_n + a.eps);
+        refill();
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live[i]) continue;
+        constexpr bool again = NC != NV;
+        if constexpr (again) constants_gate(i, cg[0]);
+        Stream8<ST> xs;
+        if (has_y) {
+          float yv[8];
+          ys[i].get(yv);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if constexpr (POST) yv[k] *= rstd_y;
+            v[i][k] = fmaf(a.alpha, v[i][k], yv[k] * cg[again ? 0 : i][k]);
+          }
+        }
+        xs.round(v[i]);
+        if (a.x_out != nullptr) xs.store(a.x_out, row * a.ldxo + col[i]);
+      }
+      float mean = 0.0f, rstd = 1.0f;
+      if (a.norm == NORM_LAYER) {
+        // Each warp's mean and centred sum of squares, then (after one barrier) those of the row:
+        // sum of squares about the row's mean = sum over warps of (theirs + n (their mean - mean)^2).
+        // As exact as a second pass over the values.
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (!live[i]) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum += v[i][k];
+        }
+        const float wmean = row_sum<true>(sum, nullptr) * my_inv;
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (!live[i]) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float d = v[i][k] - wmean;
+            ss = fmaf(d, d, ss);
+          }
+        }
+        ss = row_sum<true>(ss, nullptr);
+        if ((threadIdx.x & 31) == 0) {
+          rd[1][threadIdx.x >> 5] = wmean;
+          rd[2][threadIdx.x >> 5] = ss;
+        }
+        __syncthreads();
+        const float m = lane16 < warps ? rd[1][lane16] : 0.0f, q = lane16 < warps ? rd[2][lane16] : 0.0f;
+        mean = join(its_columns * m) * inv_n;
+        rstd = rsqrtf(join(fmaf(its_columns * (m - mean), m - mean, q)) * inv_n + a.eps);
+        refill();
+      } else if (a.norm == NORM_RMS) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (!live[i]) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
+        }
+        rstd = rsqrtf(cta_sum(ss, rd[2]) * inv_n + a.eps);
+        refill();
+      }
+      if (a.stats != nullptr && threadIdx.x == 0)
+        *reinterpret_cast<float4*>(a.stats + 4 * row) = make_float4(mean, rstd, rstd_y, 0.0f);
+      if (a.norm != NORM_NONE) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          Stream8<uint16_t> out;
+          out.q = make_uint4(0u, 0u, 0u, 0u);
+          if (live[i]) {
+            constexpr bool again = NC != NV;
+            if constexpr (again) constants_norm(i, cs[0], ch[0]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[i][k] = fmaf((v[i][k] - mean) * rstd, cs[again ? 0 : i][k], ch[again ? 0 : i][k]);
+            out.round(v[i]);
+            if (a.h != nullptr) out.store(a.h, row * a.ldh + col[i]);
+          }
+          if (a.q_codes != nullptr) norm_quantize8(a, v[i], live[i], row, col[i], nkb, G, enc);
+        }
+      }
+    }
+    if (!freed) __syncthreads();
+    refill();
+    if (++stage == a.stages) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
 }
@@ -385,17 +716,13 @@ struct NormGradArgs {
   int stages;             // row buffers of the ring
   float* seq_part;        // (chunks + batches) x 3 x cols, or null (no sums)
   float* w_part;          // chunks x 2 x cols, or null (neither dw nor dw_post)
+  int* seq_pieces;        // batches x 2: the first and the last piece that hold rows of a sequence
 };
-
-__device__ __forceinline__ int64_t norm_chunk_row(int64_t rows, int chunks, int64_t g) { return rows * g / chunks; }
 
 namespace normcfg {
 constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
 constexpr int GRAD_MAX_STAGES = 8;
 constexpr int REDUCE_ROWS = 32;
-constexpr int GRAD_SMEM = 220 * 1024;    // per SM, for its CTAs' row buffers and GRAD_OTHER each
-constexpr int GRAD_OTHER = 3584;         // a CTA's static and reserved shared memory
-constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 }  // namespace normcfg
 
 // Bytes of one row's buffer: the stream, its gradient, the gradient of h, the branch, the statistics
@@ -454,7 +781,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   using namespace normcfg;
   extern __shared__ __align__(128) uint8_t norm_rows[];
   __shared__ float red[2][32 * 8];
-  __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES];
+  __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES], vec_full;
   __shared__ int abort_flag;
   griddep_launch_dependents();
   griddep_wait();
@@ -483,6 +810,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
+    mbar_init(&vec_full, 1);
     fence_mbarrier_init();
     for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
   }
@@ -498,10 +826,12 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   float s_dh[NV][8], s_dhx[NV][8], s_ty[NV][8];  // sums over the current sequence's rows
   constexpr int NC = NV == 1 ? 1 : 0;
   float c_w[NC + 1][8], c_g[NC + 1][8], c_a[NC + 1][8];  // w (1 + scale), the gate, gate w_post
-  bool first_flush = true;
+  bool first_flush = true, seq_begins = false;
   int64_t b = -1, seq_end = r0;
 
-  // the sequence's constants of vector i
+  uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
+  const NormVectors vecs(a.gate, a.scale, nullptr, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
+  // the sequence's constants of vector i, from global memory
   auto constants = [&](int i, float (&cw)[8], float (&gt)[8], float (&ag)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) cw[k] = gt[k] = 1.0f;
@@ -524,8 +854,12 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
       for (int k = 0; k < 8; ++k) ag[k] *= gt[k];
     }
   };
-  auto flush = [&]() {
+  auto flush = [&](int64_t next_row) {
     if (a.seq_part == nullptr) return;  // no sums are asked for
+    if (threadIdx.x == 0) {
+      if (seq_begins) a.seq_pieces[2 * b] = g;
+      if (next_row >= seq_end || next_row >= a.rows) a.seq_pieces[2 * b + 1] = g;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!live[i]) continue;
@@ -562,23 +896,44 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   };
 
   int stage = 0;
-  uint32_t phase = 0u;
+  uint32_t phase = 0u, vec_phase = 0u;
   for (int64_t row = r0; row < r1; ++row) {
     bool skip = false;
     if (row >= seq_end) {
-      if (b >= 0) flush();
+      if (b >= 0) flush(row);
       b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
       if (b < 0) {  // rows without a sequence are left as they are
         seq_end = row + 1;
         skip = true;
       } else {
         seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
+        seq_begins = row == (a.offsets == nullptr ? b * a.rows_per_batch : static_cast<int64_t>(a.offsets[b])) || row == 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) s_dh[i][k] = s_dhx[i][k] = s_ty[i][k] = 0.0f;
-          if constexpr (NV == 1) {
-            if (live[0]) constants(0, c_w[0], c_g[0], c_a[0]);
+        }
+        if constexpr (NV == 1) {
+          // a barrier lies behind since the last sequence's were read
+          if (threadIdx.x == 0) {
+            mbar_arrive_expect_tx(&vec_full, vecs.bytes());
+            vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
+            vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
+          }
+          (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 83);
+          vec_phase ^= 1u;
+          if (live[0]) {
+            float v[8];
+            vecs.get(NormVectors::SCALE, vec_buf, col[0], a.mod_f32, 0.0f, c_w[0]);
+            vecs.get(NormVectors::W, vec_buf, col[0], a.mod_f32, 1.0f, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c_w[0][k] = (1.0f + c_w[0][k]) * v[k];
+            vecs.get(NormVectors::GATE, vec_buf, col[0], a.mod_f32, 1.0f, c_g[0]);
+            vecs.get(NormVectors::W_POST, vec_buf, col[0], a.mod_f32, 1.0f, c_a[0]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c_a[0][k] *= c_g[0][k];
           }
         }
       }
@@ -671,7 +1026,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
       phase ^= 1u;
     }
   }
-  if (b >= 0) flush();
+  if (b >= 0) flush(r1);
   if (a.w_part != nullptr && first_flush) {  // none of this piece's rows has a sequence
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -728,12 +1083,12 @@ __global__ void __launch_bounds__(32 * normcfg::REDUCE_ROWS) norm_grad_reduce_ke
     int64_t e = a.offsets == nullptr ? s + a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
     if (s < 0) s = 0;
     if (e > a.rows) e = a.rows;
+    // unchecked offsets may leave these unwritten: kept in range
+    int g0 = a.seq_pieces[2 * b], g1 = a.seq_pieces[2 * b + 1];
+    g0 = g0 < 0 ? 0 : g0 < a.chunks ? g0 : a.chunks - 1;
+    g1 = g1 < a.chunks ? g1 : a.chunks - 1;
     float v[3] = {0.0f, 0.0f, 0.0f};
     if (s < e) {
-      // pieces that hold rows of [s, e) (every piece has rows): from estimates
-      int g0 = static_cast<int>(s * a.chunks / a.rows), g1 = static_cast<int>((e - 1) * a.chunks / a.rows);
-      while (norm_chunk_row(a.rows, a.chunks, g0 + 1) <= s) ++g0;
-      while (g1 + 1 < a.chunks && norm_chunk_row(a.rows, a.chunks, g1 + 1) < e) ++g1;
       if (live) {
         const float* p = a.seq_part + (g0 + warp + b) * 3 * a.cols + col;
 #pragma unroll 5

@@ -140,6 +140,28 @@ def test_forward(rows, cols, B, opt):
     check_forward(x, a, b, hq=a["norm"] is not None and cols % 64 == 0)
 
 
+# enough rows that a CTA walks several of them
+MANY_ROWS = [
+    (700, 4096, 2, dict(post=True, w=True, alpha=0.8)),
+    (613, 4096, 1, dict(stream="f32", mod="f32", norm="rms", w=True)),
+    (2501, 1024, 1, dict(branch=False)),
+    (4800, 64, 3, dict(post=True, mod="f32")),
+    (5000, 8, 1, dict(mods=())),
+    (900, 2568, 4, dict(offsets=[0, 1, 1, 700, 890], stream="f32", post=True, w=True, norm="rms")),
+    (1500, 2048, 3, dict(offsets=[3, 900, 1400, 1500], w=True)),
+    (301, 8200, 1, dict(post=True)),
+    (302, 16384, 2, dict(stream="f32", w=True)),
+    (640, 4032, 2, dict(norm=None, post=True, w=True, alpha=0.5)),
+    (640, 3968, 5, dict(norm=None)),
+]
+
+
+@pytest.mark.parametrize("rows,cols,B,opt", MANY_ROWS)
+def test_forward_many_rows(rows, cols, B, opt):
+    x, a, b = make(rows, cols, B, **opt)
+    check_forward(x, a, b, hq=a["norm"] is not None and cols % 64 == 0)
+
+
 @pytest.mark.parametrize("stream", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(300, 4096), (257, 1024), (128, 192)])
 def test_forward_with_nvfp4_output(stream, rows, cols):
