@@ -1067,6 +1067,8 @@ nvfp4_status launch_norm(DeviceInfo* info, nvfp4::NormArgs a, int64_t rows, cuda
     if (stages > FWD_MAX_STAGES) stages = FWD_MAX_STAGES;
     if (stages < 1) stages = 1;
     a.chunks = static_cast<int>(chunks);
+    a.chunk_rows = a.rows / chunks;
+    a.chunk_extra = static_cast<int>(a.rows % chunks);
     a.stages = static_cast<int>(stages);
     const size_t smem = static_cast<size_t>(stages * stage + vectors);
     if (nv == 2) {
@@ -1278,6 +1280,8 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
   a.dw = g->dw;
   a.dw_post = g->dw_post;
   a.chunks = static_cast<int>(norm_chunks(in->rows, cols));
+  a.chunk_rows = in->rows / a.chunks;
+  a.chunk_extra = static_cast<int>(in->rows % a.chunks);
   if (seq || weights) {
     a.seq_part = static_cast<float*>(workspace);
     float* const w_part = a.seq_part + (a.chunks + in->batches) * 3 * cols;
@@ -1291,7 +1295,7 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
   if (st != NVFP4_OK || !(seq || weights)) return st;
   const int64_t by = !seq ? 0 : in->batches < 1024 ? in->batches : 1024;
   const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(by + 1));
-  return launch_dependent(nvfp4::norm_grad_reduce_kernel, grid, 32 * nvfp4::normcfg::REDUCE_ROWS, 0, stream, a);
+  return launch_dependent(nvfp4::norm_grad_reduce_kernel, grid, 32 * nvfp4::normcfg::REDUCE_WARPS, 0, stream, a);
 }
 
 namespace {

@@ -45,6 +45,8 @@ struct NormArgs {
   const float* q_gscale;
   float* stats;           // rows x 4: mean, rstd, rstd of the branch, 0; or null
   int chunks, stages;     // ring kernel: pieces of the rows, row buffers
+  int64_t chunk_rows;     // rows of a piece, and how many pieces have one more
+  int chunk_extra;
 };
 
 enum NormKind { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
@@ -382,7 +384,10 @@ __host__ __device__ constexpr int64_t norm_vector_bytes(int64_t cols, int mod_f3
 }
 
 __host__ __device__ constexpr int64_t norm_stage(int64_t cols, int elem, bool y) { return cols * (elem + 2 * y); }
-__device__ __forceinline__ int64_t norm_chunk_row(int64_t rows, int chunks, int64_t g) { return rows * g / chunks; }
+// First row of piece g: every piece has `each` rows, the first `extra` one more.
+__device__ __forceinline__ int64_t norm_chunk_row(int64_t each, int extra, int g) {
+  return each * g + (g < extra ? g : extra);
+}
 
 // residual_norm over many rows: a CTA walks a contiguous piece of them. Rows come through a ring of
 // row buffers, filled by bulk copies (one per tensor and row, issued by one thread `stages` rows
@@ -401,8 +406,8 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
   __shared__ __align__(8) uint64_t full[FWD_MAX_STAGES], vec_full;
   __shared__ int abort_flag;
   griddep_launch_dependents();
-  griddep_wait();
-  const int64_t r0 = norm_chunk_row(a.rows, a.chunks, blockIdx.x), r1 = norm_chunk_row(a.rows, a.chunks, blockIdx.x + 1);
+  const int g = blockIdx.x;
+  const int64_t r0 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g), r1 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g + 1);
   const bool has_y = a.y != nullptr;
   const uint32_t x_bytes = static_cast<uint32_t>(a.cols * sizeof(ST)), y_bytes = has_y ? static_cast<uint32_t>(a.cols * 2) : 0u;
   const uint32_t stage_bytes = x_bytes + y_bytes;
@@ -412,12 +417,30 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
     bulk_load(to, static_cast<const ST*>(a.x) + row * a.ldx, x_bytes, &full[stage]);
     if (has_y) bulk_load(to + x_bytes, a.y + row * a.ldy, y_bytes, &full[stage]);
   };
+  constexpr int NC = NV == 2 ? NV : 1;  // vectors whose modulation is kept
+  uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
+  const NormVectors vecs(a.gate, a.scale, a.shift, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
     mbar_init(&vec_full, 1);
     fence_mbarrier_init();
-    for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
+  }
+  griddep_wait();  // nothing before this reads or writes global memory
+  int64_t b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, r0), seq_end = r0;
+  auto fetch_vectors = [&]() {  // one thread
+    mbar_arrive_expect_tx(&vec_full, vecs.bytes());
+    vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::SHIFT, vec_buf, a.shift, b * a.ldshift, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
+  };
+  if (threadIdx.x < 32) {
+    // the vectors before the rows: behind all CTAs' first rows they would take 4 us
+    if (threadIdx.x == 0 && NC == NV && b >= 0) fetch_vectors();
+    __syncwarp();
+    if (static_cast<int>(threadIdx.x) < a.stages && r0 + threadIdx.x < r1) fetch(r0 + threadIdx.x, threadIdx.x);
   }
   const int64_t nkb = a.cols >> 4;
   if (a.q_codes != nullptr && blockIdx.x == gridDim.x - 1) {  // block scales of the rows that pad to 128 are 0
@@ -440,9 +463,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
     G = *a.q_gscale;
     enc = scale_encode_factor(G);
   }
-  constexpr int NC = NV == 2 ? NV : 1;
   float cg[NC][8], cs[NC][8], ch[NC][8];  // gate w_post, w (1 + scale), shift
-  int64_t b = -1, seq_end = r0;
   const int lane16 = threadIdx.x & 15, warps = blockDim.x >> 5;
   auto warp_columns = [&](int w) {  // columns that warp w holds
     int n = 0;
@@ -468,8 +489,6 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
     return join(lane16 < warps ? rd[lane16] : 0.0f);
   };
   // gate w_post, w (1 + scale) and shift of vector i, from the buffer (NV = 2) or from global memory
-  uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
-  const NormVectors vecs(a.gate, a.scale, a.shift, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
   auto times = [](float (&v)[8], const float (&w)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= w[k];
@@ -516,21 +535,14 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
   uint32_t phase = 0u, vec_phase = 0u;
   for (int64_t row = r0; row < r1; ++row) {
     if (row >= seq_end) {
-      b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
+      if (row != r0) b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
       if (b < 0) {  // rows without a sequence are left as they are
         seq_end = row + 1;
       } else {
         seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
         if constexpr (NC == NV) {
           // a barrier lies behind since the last sequence's were read
-          if (threadIdx.x == 0) {
-            mbar_arrive_expect_tx(&vec_full, vecs.bytes());
-            vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::SHIFT, vec_buf, a.shift, b * a.ldshift, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
-          }
+          if (threadIdx.x == 0 && row != r0) fetch_vectors();
           (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 82);
           vec_phase ^= 1u;
 #pragma unroll
@@ -712,8 +724,9 @@ struct NormGradArgs {
   int64_t lddgate, lddscale, lddshift;
   float* dw;              // cols, or null
   float* dw_post;
-  int chunks;
-  int stages;             // row buffers of the ring
+  int chunks, stages;     // pieces of the rows, row buffers
+  int64_t chunk_rows;     // rows of a piece, and how many pieces have one more
+  int chunk_extra;
   float* seq_part;        // (chunks + batches) x 3 x cols, or null (no sums)
   float* w_part;          // chunks x 2 x cols, or null (neither dw nor dw_post)
   int* seq_pieces;        // batches x 2: the first and the last piece that hold rows of a sequence
@@ -722,7 +735,7 @@ struct NormGradArgs {
 namespace normcfg {
 constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
 constexpr int GRAD_MAX_STAGES = 8;
-constexpr int REDUCE_ROWS = 32;
+constexpr int REDUCE_WARPS = 16;
 }  // namespace normcfg
 
 // Bytes of one row's buffer: the stream, its gradient, the gradient of h, the branch, the statistics
@@ -784,9 +797,8 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES], vec_full;
   __shared__ int abort_flag;
   griddep_launch_dependents();
-  griddep_wait();
   const int g = blockIdx.x;
-  const int64_t r0 = norm_chunk_row(a.rows, a.chunks, g), r1 = norm_chunk_row(a.rows, a.chunks, g + 1);
+  const int64_t r0 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g), r1 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g + 1);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   const bool has_dxo = a.dxo != nullptr, has_dh = a.dh != nullptr, has_y = a.y != nullptr;
   // the parts of a row buffer
@@ -807,12 +819,28 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
     if (has_y) bulk_load(to + at_y, a.y + row * a.ldy, half_bytes, bar);
     bulk_load(to + at_stats, a.stats + 4 * row, 16u, bar);
   };
+  uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
+  const NormVectors vecs(a.gate, a.scale, nullptr, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
     mbar_init(&vec_full, 1);
     fence_mbarrier_init();
-    for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
+  }
+  griddep_wait();  // nothing before this reads or writes global memory
+  int64_t b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, r0), seq_end = r0;
+  auto fetch_vectors = [&]() {  // one thread
+    mbar_arrive_expect_tx(&vec_full, vecs.bytes());
+    vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
+  };
+  if (threadIdx.x < 32) {
+    // the vectors before the rows: behind all CTAs' first rows they would take 4 us
+    if (threadIdx.x == 0 && NV == 1 && b >= 0) fetch_vectors();
+    __syncwarp();
+    if (static_cast<int>(threadIdx.x) < a.stages && r0 + threadIdx.x < r1) fetch(r0 + threadIdx.x, threadIdx.x);
   }
   __syncthreads();
 
@@ -827,10 +855,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   constexpr int NC = NV == 1 ? 1 : 0;
   float c_w[NC + 1][8], c_g[NC + 1][8], c_a[NC + 1][8];  // w (1 + scale), the gate, gate w_post
   bool first_flush = true, seq_begins = false;
-  int64_t b = -1, seq_end = r0;
 
-  uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
-  const NormVectors vecs(a.gate, a.scale, nullptr, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
   // the sequence's constants of vector i, from global memory
   auto constants = [&](int i, float (&cw)[8], float (&gt)[8], float (&ag)[8]) {
 #pragma unroll
@@ -900,8 +925,10 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   for (int64_t row = r0; row < r1; ++row) {
     bool skip = false;
     if (row >= seq_end) {
-      if (b >= 0) flush(row);
-      b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
+      if (row != r0) {
+        if (b >= 0) flush(row);
+        b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
+      }
       if (b < 0) {  // rows without a sequence are left as they are
         seq_end = row + 1;
         skip = true;
@@ -915,13 +942,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
         }
         if constexpr (NV == 1) {
           // a barrier lies behind since the last sequence's were read
-          if (threadIdx.x == 0) {
-            mbar_arrive_expect_tx(&vec_full, vecs.bytes());
-            vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
-            vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
-          }
+          if (threadIdx.x == 0 && row != r0) fetch_vectors();
           (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 83);
           vec_phase ^= 1u;
           if (live[0]) {
@@ -1041,22 +1062,23 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
 
 // Adds up the slots of each sequence and the pieces' weight sums. Block (x, y): columns 32 x and
 // on; y < gridDim.y - 1 takes the sequences y, y + gridDim.y - 1, ..., the last y the weights.
-// 32 warps share the slots, one column per lane, and are joined in a fixed order (warp c then adds
-// column c over the warps). With 148 to 2368 slots it is the latency of a thread's loads one after
-// another that counts: 8 warps with 4 loads in flight took 12 us for 296 slots of 2048 columns.
-__global__ void __launch_bounds__(32 * normcfg::REDUCE_ROWS) norm_grad_reduce_kernel(const NormGradArgs a) {
-  using normcfg::REDUCE_ROWS;
-  __shared__ float red[3][REDUCE_ROWS][33];
+// 16 warps share the slots, one column per lane, and are joined in a fixed order (a half-warp then adds
+// a column over the warps). With 148 to 2368 slots the kernel is bound by the latency of a thread's loads
+// one after another, and by how many blocks fit at once (32 warps at 64 registers: one per SM, five
+// waves at 4096 columns and 4 sequences).
+__global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, 4) norm_grad_reduce_kernel(const NormGradArgs a) {
+  using normcfg::REDUCE_WARPS;
+  __shared__ float red[3][REDUCE_WARPS][33];
   griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = 2 * warp + (lane >> 4);
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;        // while adding slots
-  const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + warp;        // while joining
-  const bool live = col < a.cols, last = lane == 0 && out < a.cols;
+  const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + mine;        // while joining
+  const bool live = col < a.cols, last = (lane & 15) == 0 && out < a.cols;
+  griddep_wait();
   auto total = [&](int k) {
-    float v = red[k][lane][warp];
+    float v = red[k][lane & 15][mine];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
   if (blockIdx.y == gridDim.y - 1) {
@@ -1064,7 +1086,7 @@ __global__ void __launch_bounds__(32 * normcfg::REDUCE_ROWS) norm_grad_reduce_ke
     if (live && a.w_part != nullptr) {
       const float* p = a.w_part + static_cast<int64_t>(warp) * 2 * a.cols + col;
 #pragma unroll 10
-      for (int g = warp; g < a.chunks; g += REDUCE_ROWS, p += 2 * REDUCE_ROWS * a.cols) {
+      for (int g = warp; g < a.chunks; g += REDUCE_WARPS, p += 2 * REDUCE_WARPS * a.cols) {
         s0 += p[0];
         s1 += p[a.cols];
       }
@@ -1092,7 +1114,7 @@ __global__ void __launch_bounds__(32 * normcfg::REDUCE_ROWS) norm_grad_reduce_ke
       if (live) {
         const float* p = a.seq_part + (g0 + warp + b) * 3 * a.cols + col;
 #pragma unroll 5
-        for (int g = g0 + warp; g <= g1; g += REDUCE_ROWS, p += 3 * REDUCE_ROWS * a.cols) {
+        for (int g = g0 + warp; g <= g1; g += REDUCE_WARPS, p += 3 * REDUCE_WARPS * a.cols) {
           v[0] += p[0];
           v[1] += p[a.cols];
           v[2] += p[2 * a.cols];
