@@ -122,7 +122,8 @@ __device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int 
 // A unit is what one thread does to one head: 16 bytes (interleaved pairs), two times 16 bytes
 // (the same places of both halves) or a 16-byte piece that passes through, and with
 // ROPE_HALVES_SCALAR (a number of pairs that 16 bytes do not divide) one pair or one element.
-// Threads keep their unit and walk the (row, head) pairs of the CTA.
+// Threads keep their unit and walk the (row, head) pairs of the CTA, BATCH at a time. A CTA's first
+// batch is loaded before its table is made, so the positions, the angles and x travel together.
 template <class T, int MODE>
 __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a) {
   using namespace ropecfg;
@@ -130,98 +131,113 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   constexpr int V = RV::V;
   extern __shared__ float2 rope_cs[];
   griddep_launch_dependents();
-  griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
   const int nrows = static_cast<int>(a.rows - row0 < a.rows_per_cta ? a.rows - row0 : a.rows_per_cta);
-  rope_table(a, row0, nrows, rope_cs);
-  __syncthreads();
-
   const int n = a.npairs;
   const int units = MODE == ROPE_INTERLEAVED ? a.head_dim / V
                     : MODE == ROPE_HALVES    ? n / V + (a.head_dim - 2 * n) / V
                                              : a.head_dim - n;
   const int slots = units < THREADS ? THREADS / units : 1;
   const int slot = units < THREADS ? threadIdx.x / units : 0;
-  if (slot >= slots) return;
   const int total = nrows * a.heads;
-  for (int u = threadIdx.x - slot * units; u < units; u += THREADS) {
-    const bool rotates = MODE == ROPE_INTERLEAVED ? u * (V / 2) < n : MODE == ROPE_HALVES ? u * V < n : u < n;
+  // (row, head) of this thread's j-th step, advanced without divisions
+  const int dr = slots / a.heads, dh = slots - dr * a.heads;
+  const int r_first = slot / a.heads, h_first = slot - r_first * a.heads;
+  auto advance = [&](int& r, int& h) {
+    r += dr;
+    h += dh;
+    if (h >= a.heads) {
+      h -= a.heads;
+      ++r;
+    }
+  };
+  const T* const x = static_cast<const T*>(a.x) + row0 * a.x_row;
+  T* const y = static_cast<T*>(a.y) + row0 * a.y_row;
+  int u = threadIdx.x - slot * units;
+  bool rotates;
+  int e0;  // first element of the unit within the head
+  auto unit = [&]() {
+    rotates = MODE == ROPE_INTERLEAVED ? u * (V / 2) < n : MODE == ROPE_HALVES ? u * V < n : u < n;
+    e0 = MODE == ROPE_INTERLEAVED ? u * V
+         : MODE == ROPE_HALVES    ? (rotates ? u * V : 2 * n + (u - n / V) * V)
+                                  : (rotates ? u : n + u);
+  };
+  unit();
+  const bool works = slot < slots && u < units;
+  uint4 lo[BATCH], hi[BATCH];
+  auto load = [&](int j, int r, int h) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (j + k * slots < total) {
+        const T* src = x + r * a.x_row + h * a.x_head + e0;
+        lo[k] = *reinterpret_cast<const uint4*>(src);
+        if (MODE == ROPE_HALVES && rotates) hi[k] = *reinterpret_cast<const uint4*>(src + n);
+      }
+      advance(r, h);
+    }
+  };
+  griddep_wait();  // nothing before this reads or writes global memory
+  if (MODE != ROPE_HALVES_SCALAR && works && (rotates || !a.in_place)) load(slot, r_first, h_first);
+  rope_table(a, row0, nrows, rope_cs);
+  __syncthreads();
+  if (!works) return;
+
+  for (; u < units; u += THREADS) {  // once, unless a head has more units than the CTA threads
+    unit();
     if (!rotates && a.in_place) continue;
-    // first element of the unit within the head
-    const int e0 = MODE == ROPE_INTERLEAVED ? u * V
-                   : MODE == ROPE_HALVES    ? (rotates ? u * V : 2 * n + (u - n / V) * V)
-                                            : (rotates ? u : n + u);
-    int r = slot / a.heads, h = slot - (slot / a.heads) * a.heads;
+    int r = r_first, h = h_first;
     for (int j = slot; j < total; j += BATCH * slots) {
-      const T* src[BATCH];
-      T* dst[BATCH];
-      const float2* cs[BATCH];
+      if constexpr (MODE != ROPE_HALVES_SCALAR) {
+        if (j != slot || u >= THREADS) load(j, r, h);
+      }
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        src[k] = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + h * a.x_head + e0;
-        dst[k] = static_cast<T*>(a.y) + (row0 + r) * a.y_row + h * a.y_head + e0;
-        cs[k] = rope_cs + r * n;
-        h += slots;
-        while (h >= a.heads) {
-          h -= a.heads;
-          ++r;
-        }
-      }
-      if constexpr (MODE == ROPE_HALVES_SCALAR) {
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          if (j + k * slots >= total) continue;
-          if (!rotates) {
-            *dst[k] = *src[k];
-          } else {
-            const float p = rope_f32(src[k][0]), q = rope_f32(src[k][n]);
-            const float2 c = cs[k][u];
-            rope_put(dst[k], p * c.x - q * c.y);
-            rope_put(dst[k] + n, p * c.y + q * c.x);
-          }
-        }
-      } else {
-        uint4 lo[BATCH], hi[BATCH];
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          if (j + k * slots < total) {
-            lo[k] = *reinterpret_cast<const uint4*>(src[k]);
-            if (MODE == ROPE_HALVES && rotates) hi[k] = *reinterpret_cast<const uint4*>(src[k] + n);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          if (j + k * slots >= total) continue;
-          if (rotates) {
-            float v[V];
-            RV::unpack(lo[k], v);
-            if constexpr (MODE == ROPE_INTERLEAVED) {
-#pragma unroll
-              for (int i = 0; i < V / 2; ++i) {
-                const int p = u * (V / 2) + i;
-                if (p < n) {
-                  const float2 c = cs[k][p];
-                  const float s0 = v[2 * i], s1 = v[2 * i + 1];
-                  v[2 * i] = s0 * c.x - s1 * c.y;
-                  v[2 * i + 1] = s0 * c.y + s1 * c.x;
-                }
-              }
+        if (j + k * slots < total) {
+          T* const dst = y + r * a.y_row + h * a.y_head + e0;
+          const float2* const cs = rope_cs + r * n;
+          if constexpr (MODE == ROPE_HALVES_SCALAR) {
+            const T* const src = x + r * a.x_row + h * a.x_head + e0;
+            if (!rotates) {
+              *dst = *src;
             } else {
-              float w[V];
-              RV::unpack(hi[k], w);
-#pragma unroll
-              for (int i = 0; i < V; ++i) {
-                const float2 c = cs[k][u * V + i];
-                const float s0 = v[i], s1 = w[i];
-                v[i] = s0 * c.x - s1 * c.y;
-                w[i] = s0 * c.y + s1 * c.x;
-              }
-              *reinterpret_cast<uint4*>(dst[k] + n) = RV::pack(w);
+              const float p = rope_f32(src[0]), q = rope_f32(src[n]);
+              const float2 c = cs[u];
+              rope_put(dst, p * c.x - q * c.y);
+              rope_put(dst + n, p * c.y + q * c.x);
             }
-            lo[k] = RV::pack(v);
+          } else {
+            if (rotates) {
+              float v[V];
+              RV::unpack(lo[k], v);
+              if constexpr (MODE == ROPE_INTERLEAVED) {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                  const int p = u * (V / 2) + i;
+                  if (p < n) {
+                    const float2 c = cs[p];
+                    const float s0 = v[2 * i], s1 = v[2 * i + 1];
+                    v[2 * i] = s0 * c.x - s1 * c.y;
+                    v[2 * i + 1] = s0 * c.y + s1 * c.x;
+                  }
+                }
+              } else {
+                float w[V];
+                RV::unpack(hi[k], w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                  const float2 c = cs[u * V + i];
+                  const float s0 = v[i], s1 = w[i];
+                  v[i] = s0 * c.x - s1 * c.y;
+                  w[i] = s0 * c.y + s1 * c.x;
+                }
+                *reinterpret_cast<uint4*>(dst + n) = RV::pack(w);
+              }
+              lo[k] = RV::pack(v);
+            }
+            *reinterpret_cast<uint4*>(dst) = lo[k];
           }
-          *reinterpret_cast<uint4*>(dst[k]) = lo[k];
         }
+        advance(r, h);
       }
     }
   }
