@@ -1374,12 +1374,13 @@ NVFP4_API nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t
   // rows per CTA: about two batches of 16-byte accesses per thread, a table within its limit, and
   // enough CTAs for the GPU
   int64_t r = 2 * BATCH * THREADS * 16 / (heads * head_dim * es);
-  const int64_t table = MAX_TABLE_BYTES / (n * 8);
+  a.table_pitch = static_cast<int>((n + 3) / 4 * 4);
+  const int64_t table = MAX_TABLE_BYTES / (a.table_pitch * 8);
   if (r > table) r = table;
   if (r > rows / (8 * info->sm_count)) r = rows / (8 * info->sm_count);
   if (r < 1) r = 1;
   a.rows_per_cta = static_cast<int>(r);
-  const size_t smem = static_cast<size_t>(r * n) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(r * a.table_pitch) * 2 * sizeof(float);
   const bool inter = interleaved != 0;
   return dtype == NVFP4_OUT_F32   ? launch_rope<float>(a, inter, smem, stream)
          : dtype == NVFP4_OUT_F16 ? launch_rope<__half>(a, inter, smem, stream)

@@ -42,6 +42,7 @@ struct RopeArgs {
   int inverse;
   int rows_per_cta;
   int in_place;                          // y is x: what passes through stays where it is
+  int table_pitch;                       // pairs per row of the table (npairs to the next multiple of 4)
 };
 
 template <class T>
@@ -100,9 +101,9 @@ __device__ __forceinline__ void rope_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void rope_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void rope_put(__half* p, float v) { *p = __float2half_rn(v); }
 
-// cos and sin of the pairs of this CTA's rows. `width` entries per row; those past npairs are
-// not read.
-__device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int nrows, float2* cs) {
+// cos and sin of the pairs of this CTA's rows, in two tables (a thread reads those of four pairs at a
+// time: interleaved with one another, they conflicted in shared memory's banks).
+__device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int nrows, float* cosines, float* sines) {
   for (int i = threadIdx.x; i < nrows * a.npairs; i += ropecfg::THREADS) {
     const int r = i / a.npairs, p = i - r * a.npairs;
     int ax = 0;
@@ -115,7 +116,8 @@ __device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int 
     u -= 2.0 * rint(0.5 * u);
     float s, c;
     sincospif(static_cast<float>(u), &s, &c);
-    cs[i] = make_float2(c, a.inverse ? -s : s);
+    cosines[r * a.table_pitch + p] = c;
+    sines[r * a.table_pitch + p] = a.inverse ? -s : s;
   }
 }
 
@@ -129,7 +131,9 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   using namespace ropecfg;
   using RV = RopeVec<T>;
   constexpr int V = RV::V;
-  extern __shared__ float2 rope_cs[];
+  extern __shared__ float rope_cos[];
+  float* const rope_sin = rope_cos + a.rows_per_cta * a.table_pitch;
+  constexpr int NP = MODE == ROPE_INTERLEAVED ? V / 2 : V;  // pairs of a unit
   griddep_launch_dependents();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
   const int nrows = static_cast<int>(a.rows - row0 < a.rows_per_cta ? a.rows - row0 : a.rows_per_cta);
@@ -178,14 +182,17 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   };
   griddep_wait();  // nothing before this reads or writes global memory
   if (MODE != ROPE_HALVES_SCALAR && works && (rotates || !a.in_place)) load(slot, r_first, h_first);
-  rope_table(a, row0, nrows, rope_cs);
+  rope_table(a, row0, nrows, rope_cos, rope_sin);
   __syncthreads();
   if (!works) return;
 
   for (; u < units; u += THREADS) {  // once, unless a head has more units than the CTA threads
     unit();
     if (!rotates && a.in_place) continue;
-    int r = r_first, h = h_first;
+    // the pairs' cos and sin stay in registers while the row is the same
+    float c[NP], sn[NP];
+    const bool whole = (u + 1) * NP <= n;  // else the unit's last pairs pass through
+    int r = r_first, h = h_first, of = -1;
     for (int j = slot; j < total; j += BATCH * slots) {
       if constexpr (MODE != ROPE_HALVES_SCALAR) {
         if (j != slot || u >= THREADS) load(j, r, h);
@@ -194,30 +201,49 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
       for (int k = 0; k < BATCH; ++k) {
         if (j + k * slots < total) {
           T* const dst = y + r * a.y_row + h * a.y_head + e0;
-          const float2* const cs = rope_cs + r * n;
           if constexpr (MODE == ROPE_HALVES_SCALAR) {
             const T* const src = x + r * a.x_row + h * a.x_head + e0;
             if (!rotates) {
               *dst = *src;
             } else {
               const float p = rope_f32(src[0]), q = rope_f32(src[n]);
-              const float2 c = cs[u];
-              rope_put(dst, p * c.x - q * c.y);
-              rope_put(dst + n, p * c.y + q * c.x);
+              const float c1 = rope_cos[r * a.table_pitch + u], s1 = rope_sin[r * a.table_pitch + u];
+              rope_put(dst, p * c1 - q * s1);
+              rope_put(dst + n, p * s1 + q * c1);
             }
           } else {
             if (rotates) {
+              if (r != of) {
+                of = r;
+                const float* const ct = rope_cos + r * a.table_pitch + u * NP;
+                const float* const st = rope_sin + r * a.table_pitch + u * NP;
+                if constexpr (NP % 4 == 0) {
+#pragma unroll
+                  for (int i = 0; i < NP; i += 4) {
+                    const float4 c4 = *reinterpret_cast<const float4*>(ct + i), s4 = *reinterpret_cast<const float4*>(st + i);
+                    c[i] = c4.x, c[i + 1] = c4.y, c[i + 2] = c4.z, c[i + 3] = c4.w;
+                    sn[i] = s4.x, sn[i + 1] = s4.y, sn[i + 2] = s4.z, sn[i + 3] = s4.w;
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) c[i] = ct[i], sn[i] = st[i];
+                }
+              }
               float v[V];
               RV::unpack(lo[k], v);
               if constexpr (MODE == ROPE_INTERLEAVED) {
+                auto turn = [&](int i) {
+                  const float s0 = v[2 * i], s1 = v[2 * i + 1];
+                  v[2 * i] = s0 * c[i] - s1 * sn[i];
+                  v[2 * i + 1] = s0 * sn[i] + s1 * c[i];
+                };
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i) {
-                  const int p = u * (V / 2) + i;
-                  if (p < n) {
-                    const float2 c = cs[p];
-                    const float s0 = v[2 * i], s1 = v[2 * i + 1];
-                    v[2 * i] = s0 * c.x - s1 * c.y;
-                    v[2 * i + 1] = s0 * c.y + s1 * c.x;
+                  for (int i = 0; i < NP; ++i) turn(i);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) {
+                    if (u * NP + i < n) turn(i);
                   }
                 }
               } else {
@@ -225,10 +251,9 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
                 RV::unpack(hi[k], w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                  const float2 c = cs[u * V + i];
                   const float s0 = v[i], s1 = w[i];
-                  v[i] = s0 * c.x - s1 * c.y;
-                  w[i] = s0 * c.y + s1 * c.x;
+                  v[i] = s0 * c[i] - s1 * sn[i];
+                  w[i] = s0 * sn[i] + s1 * c[i];
                 }
                 *reinterpret_cast<uint4*>(dst + n) = RV::pack(w);
               }
