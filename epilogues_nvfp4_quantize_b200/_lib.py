@@ -8,7 +8,9 @@ be loaded, every call fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -34,22 +36,6 @@ EXPORTS = (
 class _Tensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("gscale", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
-
-
-_i64, _vp, _i32, _f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
-
-
-class _NormInputs(ctypes.Structure):
-    _fields_ = [("rows", _i64), ("cols", _i64), ("batches", _i64), ("offsets", _vp), ("stream_dtype", _i32),
-                ("mod_dtype", _i32), ("norm", _i32), ("post_norm", _i32), ("residual_scale", _f32), ("eps", _f32),
-                ("x", _vp), ("ldx", _i64), ("y", _vp), ("ldy", _i64), ("gate", _vp), ("ldgate", _i64),
-                ("scale", _vp), ("ldscale", _i64), ("shift", _vp), ("ldshift", _i64), ("w_post", _vp), ("w", _vp)]
-
-
-class _NormGrads(ctypes.Structure):
-    _fields_ = [("dx_out", _vp), ("lddxo", _i64), ("dh", _vp), ("lddh", _i64), ("dx", _vp), ("lddx", _i64),
-                ("dy", _vp), ("lddy", _i64), ("dgate", _vp), ("lddgate", _i64), ("dscale", _vp), ("lddscale", _i64),
-                ("dshift", _vp), ("lddshift", _i64), ("dw", _vp), ("dw_post", _vp)]
 
 
 _lib = None
@@ -89,9 +75,9 @@ def load() -> ctypes.CDLL:
         "gemm_mxfp4_swiglu": (i32, [_Tensor, _Tensor, vp, i64, ctypes.POINTER(_Tensor), vp]),
         "nvfp4_signal_barrier": (i32, [vp, i32, i32, ctypes.c_uint32, i64, vp]),
         "gemv_nvfp4": (i32, [vp, i32, i64, i64, i32, _Tensor, vp, i32, vp, i64, vp]),
-        "residual_norm": (i32, [ctypes.POINTER(_NormInputs), vp, i64, vp, i64, ctypes.POINTER(_Tensor), vp, vp]),
+        "residual_norm": (i32, [ctypes.c_char_p, vp, i64, vp, i64, ctypes.POINTER(_Tensor), vp, vp]),
         "residual_norm_workspace_bytes": (i64, [i64, i64, i64]),
-        "residual_norm_backward": (i32, [ctypes.POINTER(_NormInputs), vp, ctypes.POINTER(_NormGrads), vp, vp]),
+        "residual_norm_backward": (i32, [ctypes.c_char_p, vp, ctypes.c_char_p, vp, vp]),
         "rope_axes": (i32, [vp, i32, i64, i64, i64, i64, i64, vp, i32, i64, i32, ctypes.POINTER(ctypes.c_int32), vp,
                             i32, i32, vp, i64, i64, vp]),
     }
@@ -362,6 +348,8 @@ class FakeQuantizeSTE(torch.autograd.Function):
 
 
 # ---- operators between the GEMMs of a layer -------------------------------------------
+# Their kernels take a few microseconds at small sizes, so the checks here ask each tensor for as
+# little as they can (every attribute of a tensor costs about 0.1 us).
 def _same_device(*tensors: Optional[torch.Tensor]) -> int:
     """Index of the one CUDA device that all given tensors are on."""
     dev = -2
@@ -396,78 +384,92 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
 ACT_SILU = 2
 
 
+def _pitch(stride, rows: int, cols: int) -> int:
+    """Row pitch from a 2-D tensor's strides. One row has no pitch, and torch may report any."""
+    return stride[0] if rows > 1 else max(stride[0], (cols + 7) // 8 * 8)
+
+
 def gemv_nvfp4(x: torch.Tensor, B: NVFP4Tensor, D: torch.Tensor, bias: Optional[torch.Tensor] = None,
                silu: bool = False, stream=None) -> torch.Tensor:
     """D = cast(f(x) (G B)^T + bias) for a few rows x (M x K, bf16 or f16) and an NVFP4 weight B
     (N x K); f is the identity or SiLU; D (M x N) is bf16, f16 or f32 (see gemv_nvfp4 in the
     header)."""
-    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16) or x.stride(1) != 1:
+    x_dtype, sx, D_dtype, sD = x.dtype, x.stride(), D.dtype, D.stride()
+    if len(sx) != 2 or sx[1] != 1 or (x_dtype is not torch.bfloat16 and x_dtype is not torch.float16):
         raise ValueError("x must be a 2-D bf16 or f16 tensor with unit column stride")
-    if D.dtype not in _OUT_KIND or D.dim() != 2 or D.stride(1) != 1:
-        raise ValueError("D must be a 2-D bf16, f16 or f32 tensor with unit column stride")
     M, K = x.shape
-    if K != B.cols or D.shape[0] != M or D.shape[1] != B.rows:
-        raise ValueError(f"x is {M} x {K}, B {B.rows} x {B.cols} and D {tuple(D.shape)}")
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (B.rows,) or not bias.is_contiguous()):
+    N = B.rows
+    if D_dtype not in _OUT_KIND or len(sD) != 2 or (sD[1] != 1 and N > 1):
+        raise ValueError("D must be a 2-D bf16, f16 or f32 tensor with unit column stride")
+    if K != B.cols or D.shape != (M, N):
+        raise ValueError(f"x is {M} x {K}, B {N} x {B.cols} and D {tuple(D.shape)}")
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous float32 tensor with one value per row of B")
     dev = _same_device(x, D, B.codes, B.sf, B.gscale, bias)
-    _call(load().gemv_nvfp4, "gemv_nvfp4", dev, stream, x.data_ptr(), _OUT_KIND[x.dtype], M, _ld(x),
-          ACT_SILU if silu else ACT_NONE, B.c(), _ptr(bias), _OUT_KIND[D.dtype], D.data_ptr(), _ld(D))
+    _call((_lib or load()).gemv_nvfp4, "gemv_nvfp4", dev, stream, x.data_ptr(), _OUT_KIND[x_dtype], M,
+          _pitch(sx, M, K), ACT_SILU if silu else ACT_NONE, B.c(), None if bias is None else bias.data_ptr(),
+          _OUT_KIND[D_dtype], D.data_ptr(), _pitch(sD, M, N))
     return D
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row pitch of a 2-D tensor. One row has no pitch, and torch may report any for it."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
-
-
 _NORMS = {None: 0, "layer": 1, "rms": 2}
-_MOD_DTYPES = (torch.bfloat16, torch.float32)
+# nvfp4_norm_inputs and nvfp4_norm_grads of the header, packed in one step (a ctypes structure of as
+# many fields takes 3 us to fill)
+_NORM_INPUTS = struct.Struct("@3qP4i2f" + "Pq" * 5 + "2P")
+_NORM_GRADS = struct.Struct("@" + "Pq" * 7 + "2P")
 
 
 def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
     """Pointer and row pitch of an optional 2-D tensor of the given shape and type."""
     if t is None:
-        return None, 0
-    if t.shape != shape or t.dtype != dtype or t.stride(1) != 1:
+        return 0, 0
+    s = t.stride()
+    if t.dtype is not dtype or t.shape != shape or s[1] != 1:
         raise ValueError(f"{name} must be a {shape[0]} x {shape[1]} {dtype} tensor with unit column stride")
-    return t.data_ptr(), _ld(t)
+    return t.data_ptr(), _pitch(s, *shape)
 
 
 def _vector(t: Optional[torch.Tensor], name: str, cols: int):
     if t is None:
-        return None
-    if t.shape != (cols,) or t.dtype != torch.float32 or not t.is_contiguous():
+        return 0
+    if t.dtype is not torch.float32 or t.shape != (cols,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {cols} values")
     return t.data_ptr()
 
 
 def _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches):
-    if x.dim() != 2 or x.dtype not in _MOD_DTYPES or x.stride(1) != 1:
+    """The inputs checked and packed, and the modulation tensors' shape."""
+    x_dtype, sx, x_shape = x.dtype, x.stride(), x.shape
+    if len(sx) != 2 or sx[1] != 1 or (x_dtype is not torch.bfloat16 and x_dtype is not torch.float32):
         raise ValueError("the stream must be a 2-D bf16 or float32 tensor with unit column stride")
     if norm not in _NORMS:
         raise ValueError('norm must be "layer", "rms" or None')
-    rows, cols = x.shape
-    mods = [m for m in (gate, scale, shift) if m is not None]
+    rows, cols = x_shape
+    mod = gate if gate is not None else scale if scale is not None else shift
     if offsets is not None:
-        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+        if offsets.dtype is not torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
             raise ValueError("offsets must be a contiguous 1-D int32 tensor of batches + 1 values")
-        if batches is not None and batches != offsets.shape[0] - 1:
+        n = offsets.shape[0] - 1
+        if batches is not None and batches != n:
             raise ValueError("batches does not agree with offsets")
-        batches = offsets.shape[0] - 1
+        batches = n
     elif batches is None:
-        batches = mods[0].shape[0] if mods else 1
-    mod_dtype = mods[0].dtype if mods else torch.float32
-    if mod_dtype not in _MOD_DTYPES:
+        batches = mod.shape[0] if mod is not None else 1
+    mod_dtype = mod.dtype if mod is not None else torch.float32
+    if mod_dtype is not torch.bfloat16 and mod_dtype is not torch.float32:
         raise ValueError("gate, scale and shift must be bf16 or float32")
     shape = (batches, cols)
-    pg, lg = _matrix(gate, "gate", shape, mod_dtype)
-    ps, ls = _matrix(scale, "scale", shape, mod_dtype)
-    ph, lh = _matrix(shift, "shift", shape, mod_dtype)
-    py, ly = _matrix(y, "y", x.shape, torch.bfloat16)
-    return _NormInputs(rows, cols, batches, _ptr(offsets), _OUT_KIND[x.dtype], _OUT_KIND[mod_dtype], _NORMS[norm],
-                       int(post_norm), residual_scale, eps, x.data_ptr(), _ld(x), py, ly, pg, lg, ps, ls, ph, lh,
-                       _vector(w_post, "w_post", cols), _vector(w, "w", cols))
+    return _NORM_INPUTS.pack(
+        rows, cols, batches, 0 if offsets is None else offsets.data_ptr(), _OUT_KIND[x_dtype], _OUT_KIND[mod_dtype],
+        _NORMS[norm], post_norm, residual_scale, eps, x.data_ptr(), _pitch(sx, rows, cols),
+        *_matrix(y, "y", x_shape, torch.bfloat16), *_matrix(gate, "gate", shape, mod_dtype),
+        *_matrix(scale, "scale", shape, mod_dtype), *_matrix(shift, "shift", shape, mod_dtype),
+        _vector(w_post, "w_post", cols), _vector(w, "w", cols)), shape
+
+
+def _stats(stats, rows):
+    if stats is not None and (stats.dtype is not torch.float32 or stats.shape != (rows, 4) or not stats.is_contiguous()):
+        raise ValueError("stats must be a contiguous rows x 4 float32 tensor")
 
 
 def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, hq: Optional[NVFP4Tensor] = None, *,
@@ -488,22 +490,17 @@ def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, hq: Optiona
     None are not written. Returns (x_out, h, hq)."""
     dev = _same_device(x, h, y, x_out, gate, w_post, w, scale, shift, offsets, stats,
                        *((hq.codes, hq.sf, hq.gscale) if hq is not None else ()))
-    a = _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
-    pxo, lxo = _matrix(x_out, "x_out", x.shape, x.dtype)
-    ph, lh = _matrix(h, "h", x.shape, torch.bfloat16)
-    _stats(stats, x.shape[0])
-    _call(load().residual_norm, "residual_norm", dev, stream, a, pxo, lxo, ph, lh,
-          ctypes.pointer(hq.c()) if hq is not None else None, _ptr(stats))
+    a, _ = _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
+    shape = x.shape
+    _stats(stats, shape[0])
+    _call((_lib or load()).residual_norm, "residual_norm", dev, stream, a, *_matrix(x_out, "x_out", shape, x.dtype),
+          *_matrix(h, "h", shape, torch.bfloat16), ctypes.pointer(hq.c()) if hq is not None else None,
+          None if stats is None else stats.data_ptr())
     return x_out, h, hq
 
 
-def _stats(stats, rows):
-    if stats is not None and (stats.shape != (rows, 4) or stats.dtype != torch.float32 or not stats.is_contiguous()):
-        raise ValueError("stats must be a contiguous rows x 4 float32 tensor")
-
-
 def residual_norm_workspace_bytes(rows: int, cols: int, batches: int) -> int:
-    return int(load().residual_norm_workspace_bytes(rows, cols, batches))
+    return int((_lib or load()).residual_norm_workspace_bytes(rows, cols, batches))
 
 
 def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: Optional[torch.Tensor] = None,
@@ -522,27 +519,28 @@ def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: 
     dx, dy (as x, y), dgate, dscale, dshift (batches x cols float32), dw and dw_post (cols float32)
     are given; they are overwritten. x_out is the stream that the forward call stored, stats what it
     wrote there (see residual_norm_backward in the header)."""
-    seq = [t for t in (dgate, dscale, dshift) if t is not None]
     dev = _same_device(x_out, stats, dx_out, dh, y, gate, w_post, w, scale, offsets, dx, dy, dgate, dscale, dshift,
                        dw, dw_post, workspace)
-    if batches is None and offsets is None and gate is None and scale is None and seq:
-        batches = seq[0].shape[0]
-    a = _norm_inputs(x_out, y, gate, scale, None, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
-    _stats(stats, x_out.shape[0])
-    shape = (a.batches, a.cols)
-    g = _NormGrads(*_matrix(dx_out, "dx_out", x_out.shape, x_out.dtype), *_matrix(dh, "dh", x_out.shape, torch.bfloat16),
-                   *_matrix(dx, "dx", x_out.shape, x_out.dtype), *_matrix(dy, "dy", x_out.shape, torch.bfloat16),
-                   *_matrix(dgate, "dgate", shape, torch.float32), *_matrix(dscale, "dscale", shape, torch.float32),
-                   *_matrix(dshift, "dshift", shape, torch.float32), _vector(dw, "dw", a.cols),
-                   _vector(dw_post, "dw_post", a.cols))
-    if seq or dw is not None or dw_post is not None:
-        need = residual_norm_workspace_bytes(*x_out.shape, a.batches)
+    seq = dgate if dgate is not None else dscale if dscale is not None else dshift
+    if batches is None and offsets is None and gate is None and scale is None and seq is not None:
+        batches = seq.shape[0]
+    a, shape = _norm_inputs(x_out, y, gate, scale, None, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
+    full, dtype, bf16, f32 = x_out.shape, x_out.dtype, torch.bfloat16, torch.float32
+    rows, cols = full
+    _stats(stats, rows)
+    g = _NORM_GRADS.pack(*_matrix(dx_out, "dx_out", full, dtype), *_matrix(dh, "dh", full, bf16),
+                         *_matrix(dx, "dx", full, dtype), *_matrix(dy, "dy", full, bf16),
+                         *_matrix(dgate, "dgate", shape, f32), *_matrix(dscale, "dscale", shape, f32),
+                         *_matrix(dshift, "dshift", shape, f32), _vector(dw, "dw", cols),
+                         _vector(dw_post, "dw_post", cols))
+    if seq is not None or dw is not None or dw_post is not None:
+        need = residual_norm_workspace_bytes(rows, cols, shape[0])
         if workspace is None:
             workspace = torch.empty((need,), dtype=torch.uint8, device=x_out.device)
         elif workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
-    _call(load().residual_norm_backward, "residual_norm_backward", dev, stream, a, stats.data_ptr(), g,
-          _ptr(workspace))
+    _call((_lib or load()).residual_norm_backward, "residual_norm_backward", dev, stream, a, stats.data_ptr(), g,
+          None if workspace is None else workspace.data_ptr())
 
 
 def _rows_of_16_bytes(t: torch.Tensor) -> torch.Tensor:
@@ -622,30 +620,37 @@ def rope_frequencies(pairs, theta: float = 10000.0, device="cuda") -> torch.Tens
     return torch.cat([theta ** (-torch.arange(n, dtype=torch.float64) / n) for n in pairs]).to(device)
 
 
+@functools.lru_cache(maxsize=256)
+def _axis_pairs(pairs: tuple):
+    return (ctypes.c_int32 * len(pairs))(*pairs), len(pairs), sum(pairs)
+
+
 def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pairs, y: Optional[torch.Tensor] = None,
               interleaved: bool = True, inverse: bool = False, stream=None) -> torch.Tensor:
     """Rotary positions on heads x (rows x heads x head_dim; bf16, f16 or f32) into y, which may be
     x itself (None: a new contiguous tensor). positions: rows x axes, int32 or float32; pairs: how
     many pairs each axis turns; freqs: one float64 per pair (rope_frequencies). inverse: the
     opposite rotation, which is also the gradient (see rope_axes in the header)."""
-    if x.dim() != 3 or x.dtype not in _OUT_KIND or x.stride(2) != 1:
+    dtype, sx, shape = x.dtype, x.stride(), x.shape
+    if len(sx) != 3 or sx[2] != 1 or dtype not in _OUT_KIND:
         raise ValueError("x must be a rows x heads x head_dim tensor (bf16, f16 or f32) with unit last stride")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif y.shape != x.shape or y.dtype != x.dtype or y.stride(2) != 1:
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    sy = y.stride()
+    if y.shape != shape or y.dtype is not dtype or sy[2] != 1:
         raise ValueError("y must have x's shape and type and unit last stride")
-    rows, heads, head_dim = x.shape
-    if positions.dim() != 2 or positions.shape != (rows, len(pairs)) or positions.dtype not in (
-            torch.int32, torch.float32) or (len(pairs) > 1 and positions.stride(1) != 1):
+    rows, heads, head_dim = shape
+    c_pairs, axes, n = _axis_pairs(tuple(pairs))
+    p_dtype, sp = positions.dtype, positions.stride()
+    if positions.shape != (rows, axes) or (p_dtype is not torch.int32 and p_dtype is not torch.float32) or (
+            axes > 1 and sp[1] != 1):
         raise ValueError("positions must be rows x axes int32 or float32 with unit column stride")
-    if freqs.dtype != torch.float64 or freqs.shape != (sum(pairs),) or not freqs.is_contiguous():
+    if freqs.dtype is not torch.float64 or freqs.shape != (n,) or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 tensor with one value per pair")
     dev = _same_device(x, y, positions, freqs)
-    ldpos = positions.stride(0) if rows > 1 else len(pairs)
-    _call(load().rope_axes, "rope_axes", dev, stream, x.data_ptr(), _OUT_KIND[x.dtype], rows, heads, head_dim,
-          x.stride(0), x.stride(1), positions.data_ptr(), int(positions.dtype == torch.float32), ldpos, len(pairs),
-          (ctypes.c_int32 * len(pairs))(*pairs), freqs.data_ptr(), int(interleaved), int(inverse), y.data_ptr(),
-          y.stride(0), y.stride(1))
+    _call((_lib or load()).rope_axes, "rope_axes", dev, stream, x.data_ptr(), _OUT_KIND[dtype], rows, heads, head_dim,
+          sx[0], sx[1], positions.data_ptr(), p_dtype is torch.float32, sp[0] if rows > 1 else axes, axes, c_pairs,
+          freqs.data_ptr(), interleaved, inverse, y.data_ptr(), sy[0], sy[1])
     return y
 
 

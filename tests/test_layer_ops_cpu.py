@@ -125,11 +125,16 @@ def test_gemv_argument_checks(lib):
     assert call(D=17) == MISALIGNED and call(D=18, ot=2) == MISALIGNED
 
 
+NORM_FIELDS = ("rows cols batches offsets stream_dtype mod_dtype norm post_norm residual_scale eps x ldx y ldy gate "
+               "ldgate scale ldscale shift ldshift w_post w").split()
+GRAD_FIELDS = "dx_out lddxo dh lddh dx lddx dy lddy dgate lddgate dscale lddscale dshift lddshift dw dw_post".split()
+
+
 def _norm(**k):
-    a = dict(rows=4, cols=64, batches=2, offsets=None, stream_dtype=0, mod_dtype=0, norm=1, post_norm=0,
-             residual_scale=1.0, eps=1e-6, x=16, ldx=64)
+    a = dict(rows=4, cols=64, batches=2, norm=1, residual_scale=1.0, eps=1e-6, x=16, ldx=64)
     a.update(k)
-    return _lib._NormInputs(**a)
+    assert set(a) <= set(NORM_FIELDS)
+    return _lib._NORM_INPUTS.pack(*(a.get(f) or 0 for f in NORM_FIELDS))
 
 
 def test_residual_norm_argument_checks(lib):
@@ -163,7 +168,9 @@ def test_residual_norm_backward_argument_checks(lib):
     def call(stats=16, ws=16, i=None, **k):
         g = dict(dx_out=16, lddxo=64, dh=16, lddh=64, dx=16, lddx=64)
         g.update(k)
-        return lib.residual_norm_backward(_norm(**(i or {})), stats, _lib._NormGrads(**g), ws, None)
+        assert set(g) <= set(GRAD_FIELDS)
+        packed = _lib._NORM_GRADS.pack(*(g.get(f) or 0 for f in GRAD_FIELDS))
+        return lib.residual_norm_backward(_norm(**(i or {})), stats, packed, ws, None)
 
     assert lib.residual_norm_backward(_norm(), 16, None, 16, None) == INVALID
     assert call(stats=None) == INVALID and call(dx_out=None, dh=None) == INVALID and call(dx=None) == INVALID
@@ -223,10 +230,11 @@ def test_python_calls_refuse_wrong_tensors(lib):
         a.update(k)
         return _lib._norm_inputs(**a)
 
-    assert norm_inputs().batches == 1
+    assert norm_inputs()[1] == (1, 64)
     mod = torch.zeros(2, 192, dtype=bf)
-    a = norm_inputs(y=x, gate=mod[:, :64], scale=mod[:, 64:128], shift=mod[:, 128:])
-    assert (a.batches, a.ldgate, a.mod_dtype) == (2, 192, 0)
+    packed, shape = norm_inputs(y=x, gate=mod[:, :64], scale=mod[:, 64:128], shift=mod[:, 128:])
+    a = dict(zip(NORM_FIELDS, _lib._NORM_INPUTS.unpack(packed)))
+    assert shape == (2, 64) and (a["batches"], a["ldgate"], a["mod_dtype"]) == (2, 192, 0)
     for bad in (dict(x=x.half()), dict(x=x[0]), dict(norm="group"), dict(y=x.float()), dict(y=x[:, :32]),
                 dict(scale=mod[:, :32]), dict(scale=mod[:, :64], shift=mod[:, :64].float()), dict(scale=mod[:, :64].half()),
                 dict(w=torch.zeros(64, dtype=bf)), dict(w_post=torch.zeros(32)),
