@@ -162,7 +162,6 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
   uint8_t* xs = reinterpret_cast<uint8_t*>(amax + 8 * NT);                     // [tokens][pitch]
 
   griddep_launch_dependents();
-  griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) & (cluster - 1);
   const int cid = static_cast<int>(blockIdx.x) >> a.cluster_log2;
@@ -184,6 +183,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     for (int v = ((warp & ((1 << xwarps_log2) - 1)) << 5) + lane; v < xvecs; v += 32 << xwarps_log2)
       body(v, reinterpret_cast<uint4*>(row + (v >> 4) * 256 + (v & 3) * 64 + ((v >> 2) & 3) * 16));
   };
+  griddep_wait();  // nothing before this reads or writes global memory
   {
     const uint16_t* row = a.x + (m0 + xm) * a.ldx + k0;
     each_vector([&](int v, uint4* p) { copy_async16(smem_u32(p), v < vecs ? row + 8 * v : a.x, v < vecs ? 16 : 0); });
@@ -244,11 +244,14 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     copy_async_commit();
   };
   seek();
+  // Some steps of weights travel with x, the others follow when x is done: the copies of DEPTH steps
+  // hold a warp up for 5 us, until most of them have arrived.
+  constexpr int FIRST = 4;
 #pragma unroll
-  for (int j = 0; j < DEPTH; ++j) load(my_ring + j * SLOT);
+  for (int j = 0; j < FIRST; ++j) load(my_ring + j * SLOT);
 
   // ---- x to f16, each row by its power of two ---------------------------------------------
-  copy_async_wait<DEPTH>();
+  copy_async_wait<FIRST>();
   if (a.x_f16 && !a.silu) {  // f16 needs no factor
     if (tid < 8 * NT) inv[tid] = 1.0f;
   } else {
@@ -296,6 +299,8 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
       });
     }
   }
+#pragma unroll
+  for (int j = FIRST; j < DEPTH; ++j) load(my_ring + j * SLOT);
   __syncthreads();
 
   // ---- products -------------------------------------------------------------------------
