@@ -1371,14 +1371,28 @@ NVFP4_API nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t
   a.npairs = static_cast<int>(n);
   a.inverse = inverse;
   a.in_place = x == y;
-  // rows per CTA: about two batches of 16-byte accesses per thread, a table within its limit, and
-  // enough CTAs for the GPU
-  int64_t r = 2 * BATCH * THREADS * 16 / (heads * head_dim * es);
+  // Rows per CTA: as many as fill a thread's batches best, up to two batches (a batch that is half empty
+  // was measured at 39.6 us where full ones take 33.4), within the table's limit and with enough CTAs
+  // for the GPU.
   a.table_pitch = static_cast<int>((n + 3) / 4 * 4);
-  const int64_t table = MAX_TABLE_BYTES / (a.table_pitch * 8);
-  if (r > table) r = table;
-  if (r > rows / (8 * info->sm_count)) r = rows / (8 * info->sm_count);
-  if (r < 1) r = 1;
+  int64_t most = MAX_TABLE_BYTES / (a.table_pitch * 8);
+  if (most > rows / (8 * info->sm_count)) most = rows / (8 * info->sm_count);
+  const int64_t vec = 16 / es;
+  const int64_t units = interleaved        ? head_dim / vec
+                        : n % vec == 0 ? n / vec + (head_dim - 2 * n) / vec
+                                           : head_dim - n;
+  const int64_t slots = units < THREADS ? THREADS / units : 1;
+  int64_t r = 1;
+  double best = 0.0;
+  for (int64_t i = 1; i <= most; ++i) {
+    const int64_t batches = ((i * heads + slots - 1) / slots + BATCH - 1) / BATCH;
+    if (batches > 2) break;
+    const double full = static_cast<double>(i * heads) / static_cast<double>(slots * BATCH * batches);
+    if (full >= best) {
+      best = full;
+      r = i;
+    }
+  }
   a.rows_per_cta = static_cast<int>(r);
   const size_t smem = static_cast<size_t>(r * a.table_pitch) * 2 * sizeof(float);
   const bool inter = interleaved != 0;
