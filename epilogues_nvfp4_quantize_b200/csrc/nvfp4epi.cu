@@ -1382,12 +1382,13 @@ NVFP4_API nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t
                         : n % vec == 0 ? n / vec + (head_dim - 2 * n) / vec
                                            : head_dim - n;
   const int64_t slots = units < THREADS ? THREADS / units : 1;
+  const int64_t batch = !interleaved && n % vec == 0 ? BATCH_HALVES : BATCH;
   int64_t r = 1;
   double best = 0.0;
   for (int64_t i = 1; i <= most; ++i) {
-    const int64_t batches = ((i * heads + slots - 1) / slots + BATCH - 1) / BATCH;
+    const int64_t batches = ((i * heads + slots - 1) / slots + batch - 1) / batch;
     if (batches > 2) break;
-    const double full = static_cast<double>(i * heads) / static_cast<double>(slots * BATCH * batches);
+    const double full = static_cast<double>(i * heads) / static_cast<double>(slots * batch * batches);
     if (full >= best) {
       best = full;
       r = i;

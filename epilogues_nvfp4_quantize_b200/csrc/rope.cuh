@@ -19,8 +19,9 @@ namespace nvfp4 {
 
 namespace ropecfg {
 constexpr int THREADS = 256;
-constexpr int BATCH = 6;        // heads in flight per thread (of 2, 4, 6 and 8, with the best rows per CTA
-                                // for each: 23.0, 21.8, 21.7, 22.7 us on 4096 x 24 x 256 in bf16)
+// Heads in flight per thread (of 2, 4, 6 and 8, with the best rows per CTA for each: 23.0, 21.8, 21.7,
+// 22.7 us on 4096 x 24 x 256 in bf16); half as many where a head takes two accesses.
+constexpr int BATCH = 6, BATCH_HALVES = 3;
 constexpr int MAX_AXES = 4;
 constexpr int MAX_HEAD_DIM = 1024;
 constexpr int MAX_TABLE_BYTES = 16384;  // cos/sin pairs of a CTA's rows
@@ -125,7 +126,7 @@ __device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int 
 // A unit is what one thread does to one head: 16 bytes (interleaved pairs), two times 16 bytes
 // (the same places of both halves) or a 16-byte piece that passes through, and with
 // ROPE_HALVES_SCALAR (a number of pairs that 16 bytes do not divide) one pair or one element.
-// Threads keep their unit and walk the (row, head) pairs of the CTA, BATCH at a time. A CTA's first
+// Threads keep their unit and walk the (row, head) pairs of the CTA, a batch at a time. A CTA's first
 // batch is loaded before its table is made, so the positions, the angles and x travel together.
 template <class T, int MODE>
 __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a) {
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   constexpr int V = RV::V;
   extern __shared__ float rope_cos[];
   float* const rope_sin = rope_cos + a.rows_per_cta * a.table_pitch;
+  constexpr int B = MODE == ROPE_HALVES ? BATCH_HALVES : BATCH;
   constexpr int NP = MODE == ROPE_INTERLEAVED ? V / 2 : V;  // pairs of a unit
   griddep_launch_dependents();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
@@ -169,10 +171,10 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   };
   unit();
   const bool works = slot < slots && u < units;
-  uint4 lo[BATCH], hi[BATCH];
+  uint4 lo[B], hi[B];
   auto load = [&](int j, int r, int h) {
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
+    for (int k = 0; k < B; ++k) {
       if (j + k * slots < total) {
         const T* src = x + r * a.x_row + h * a.x_head + e0;
         lo[k] = *reinterpret_cast<const uint4*>(src);
@@ -194,12 +196,12 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
     float c[NP], sn[NP];
     const bool whole = (u + 1) * NP <= n;  // else the unit's last pairs pass through
     int r = r_first, h = h_first, of = -1;
-    for (int j = slot; j < total; j += BATCH * slots) {
+    for (int j = slot; j < total; j += B * slots) {
       if constexpr (MODE != ROPE_HALVES_SCALAR) {
         if (j != slot || u >= THREADS) load(j, r, h);
       }
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
+      for (int k = 0; k < B; ++k) {
         if (j + k * slots < total) {
           T* const dst = y + r * a.y_row + h * a.y_head + e0;
           if constexpr (MODE == ROPE_HALVES_SCALAR) {
