@@ -46,7 +46,7 @@ struct DeviceInfo {
   // one CTA per SM)
   int gemv_clusters[4] = {};
   bool gemv_attr_set[2] = {};
-  bool norm_attr_set[8] = {};        // residual_norm_ring_kernel, by stream type, NV and POST
+  int norm_regs[8] = {};             // registers of residual_norm_ring_kernel, by stream type, NV and POST
   bool norm_grad_attr_set[12] = {};  // residual_norm_grad_kernel, by stream type, NV and POST
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -1030,54 +1030,59 @@ nvfp4_status check_norm(const nvfp4_norm_inputs* in) {
   return NVFP4_OK;
 }
 
+// The ring kernel for many rows: as many CTAs per SM as its registers allow, as long as each has a few
+// row buffers, and a piece of rows for each. NVFP4_ERR_UNSUPPORTED_SHAPE: too few rows for it.
 template <class ST, int NV, bool POST>
-nvfp4_status launch_norm_ring(DeviceInfo* info, const nvfp4::NormArgs& a, int threads, size_t smem, cudaStream_t stream) {
+nvfp4_status launch_norm_ring(DeviceInfo* info, nvfp4::NormArgs a, cudaStream_t stream) {
+  using namespace nvfp4::normcfg;
   auto kern = nvfp4::residual_norm_ring_kernel<ST, NV, POST>;
+  int regs;
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    bool& set = info->norm_attr_set[(sizeof(ST) == 4) + 2 * (NV == 4) + 4 * POST];
-    if (!set) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, nvfp4::normcfg::SMEM) != cudaSuccess)
+    int& known = info->norm_regs[(sizeof(ST) == 4) + 2 * (NV == 4) + 4 * POST];
+    if (known == 0) {
+      cudaFuncAttributes fa;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess ||
+          cudaFuncGetAttributes(&fa, kern) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-      set = true;
+      known = (fa.numRegs + 7) / 8 * 8;
     }
+    regs = known;
   }
-  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)), threads, smem, stream, a);
+  const int64_t vecs = a.cols / 8;
+  const int threads = static_cast<int>((vecs + 32 * NV - 1) / (32 * NV) * 32);
+  const int64_t vectors =
+      NV == 2 ? nvfp4::norm_vector_bytes(a.cols, a.mod_f32,
+                                         (a.gate != nullptr) + (a.scale != nullptr) + (a.shift != nullptr),
+                                         (a.w_post != nullptr) + (a.w != nullptr))
+              : 0;
+  const int64_t stage = nvfp4::norm_stage(a.cols, sizeof(ST), a.y != nullptr);
+  int per_sm = 65536 / (regs * threads);
+  if (per_sm > 16) per_sm = 16;
+  int64_t stages = 0;
+  for (; per_sm >= 1; --per_sm) {
+    stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;
+    if (stages >= 3 || per_sm == 1) break;
+  }
+  const int64_t chunks = static_cast<int64_t>(info->sm_count) * per_sm;
+  if (per_sm < 1 || stages < 1 || a.rows < RING_ROWS * chunks) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (stages > FWD_MAX_STAGES) stages = FWD_MAX_STAGES;
+  a.chunks = static_cast<int>(chunks);
+  a.chunk_rows = a.rows / chunks;
+  a.chunk_extra = static_cast<int>(a.rows % chunks);
+  a.stages = static_cast<int>(stages);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(chunks)), threads,
+                          static_cast<size_t>(stages * stage + vectors), stream, a);
 }
 
 // `rows`: with the rows that pad an NVFP4 output's block scales.
 template <class ST>
-nvfp4_status launch_norm(DeviceInfo* info, nvfp4::NormArgs a, int64_t rows, cudaStream_t stream) {
-  using namespace nvfp4::normcfg;
+nvfp4_status launch_norm(DeviceInfo* info, const nvfp4::NormArgs& a, int64_t rows, cudaStream_t stream) {
   const int64_t vecs = a.cols / 8;
-  // the ring kernel: CTAs that share an SM, and pieces of rows for all of them
-  const int nv = vecs <= 1024 ? 2 : 4;
-  const int threads = static_cast<int>((vecs + 32 * nv - 1) / (32 * nv) * 32);
-  int per_sm = FWD_THREADS / threads;
-  if (per_sm > 16) per_sm = 16;
-  const int64_t chunks = static_cast<int64_t>(info->sm_count) * per_sm;
-  if (a.rows >= RING_ROWS * chunks) {
-    const int64_t stage = nvfp4::norm_stage(a.cols, sizeof(ST), a.y != nullptr);
-    const int64_t vectors =
-        nv == 2 ? nvfp4::norm_vector_bytes(a.cols, a.mod_f32,
-                                           (a.gate != nullptr) + (a.scale != nullptr) + (a.shift != nullptr),
-                                           (a.w_post != nullptr) + (a.w != nullptr))
-                : 0;
-    int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // the largest size leaves room for one
-    if (stages > FWD_MAX_STAGES) stages = FWD_MAX_STAGES;
-    if (stages < 1) stages = 1;
-    a.chunks = static_cast<int>(chunks);
-    a.chunk_rows = a.rows / chunks;
-    a.chunk_extra = static_cast<int>(a.rows % chunks);
-    a.stages = static_cast<int>(stages);
-    const size_t smem = static_cast<size_t>(stages * stage + vectors);
-    if (nv == 2) {
-      return a.post ? launch_norm_ring<ST, 2, true>(info, a, threads, smem, stream)
-                    : launch_norm_ring<ST, 2, false>(info, a, threads, smem, stream);
-    }
-    return a.post ? launch_norm_ring<ST, 4, true>(info, a, threads, smem, stream)
-                  : launch_norm_ring<ST, 4, false>(info, a, threads, smem, stream);
-  }
+  const nvfp4_status st =
+      vecs <= 1024 ? (a.post ? launch_norm_ring<ST, 2, true>(info, a, stream) : launch_norm_ring<ST, 2, false>(info, a, stream))
+                   : (a.post ? launch_norm_ring<ST, 4, true>(info, a, stream) : launch_norm_ring<ST, 4, false>(info, a, stream));
+  if (st != NVFP4_ERR_UNSUPPORTED_SHAPE) return st;
   if (vecs <= 128) {  // a warp per row, four rows per CTA
     auto kern = vecs <= 32   ? nvfp4::residual_norm_kernel<ST, 1, true>
                 : vecs <= 64 ? nvfp4::residual_norm_kernel<ST, 2, true>

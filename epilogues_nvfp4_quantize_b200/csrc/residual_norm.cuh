@@ -340,7 +340,6 @@ __global__ void __launch_bounds__(ONE_WARP ? 128 : 1024) residual_norm_kernel(co
 }
 
 namespace normcfg {
-constexpr int FWD_THREADS = 512;         // threads per SM that the ring kernel's registers allow
 constexpr int FWD_MAX_STAGES = 8;
 constexpr int RING_ROWS = 2;             // rows per CTA from which the ring kernel is taken
 constexpr int SMEM = 220 * 1024;         // per SM, for its CTAs' row buffers and SMEM_OTHER each
