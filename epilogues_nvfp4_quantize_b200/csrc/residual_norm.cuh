@@ -389,7 +389,7 @@ __device__ __forceinline__ int64_t norm_chunk_row(int64_t each, int extra, int g
 }
 
 // residual_norm over many rows: a CTA walks a contiguous piece of them. Rows come through a ring of
-// row buffers, filled by bulk copies (one per tensor and row, issued by one thread `stages` rows
+// row buffers, filled by bulk copies (one per tensor and row, issued by one warp `stages` rows
 // ahead), so coming rows are in flight while a row is reduced. A row's first barrier also frees its
 // buffer: every thread has read its values by then. Thread t holds the eight columns at 8 (t + i
 // threads), i < NV; with NV = 2 the sequence's modulation stays in registers, else it is read again for
@@ -410,11 +410,16 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
   const bool has_y = a.y != nullptr;
   const uint32_t x_bytes = static_cast<uint32_t>(a.cols * sizeof(ST)), y_bytes = has_y ? static_cast<uint32_t>(a.cols * 2) : 0u;
   const uint32_t stage_bytes = x_bytes + y_bytes;
-  auto fetch = [&](int64_t row, int stage) {  // one thread
-    uint8_t* to = norm_rows + stage * stage_bytes;
-    mbar_arrive_expect_tx(&full[stage], stage_bytes);
-    bulk_load(to, static_cast<const ST*>(a.x) + row * a.ldx, x_bytes, &full[stage]);
-    if (has_y) bulk_load(to + x_bytes, a.y + row * a.ldy, y_bytes, &full[stage]);
+  // Warp 0 fetches a row, one lane per tensor: what a lane copies is set once. (One thread that issued a
+  // row's copies one after another held the CTA up: 650 of the gradient's 2600 cycles per row.)
+  const int lane = threadIdx.x & 31;
+  const uint8_t* const src = static_cast<const uint8_t*>(lane == 0 ? a.x : static_cast<const void*>(a.y));
+  const int64_t src_pitch = lane == 0 ? a.ldx * static_cast<int64_t>(sizeof(ST)) : a.ldy * 2;
+  const uint32_t src_bytes = lane == 0 ? x_bytes : lane == 1 ? y_bytes : 0u, src_at = lane == 0 ? 0u : x_bytes;
+  auto fetch = [&](int64_t row, int stage) {  // warp 0
+    if (lane == 0) mbar_arrive_expect_tx(&full[stage], stage_bytes);
+    __syncwarp();
+    if (src_bytes != 0u) bulk_load(norm_rows + stage * stage_bytes + src_at, src + row * src_pitch, src_bytes, &full[stage]);
   };
   constexpr int NC = NV == 2 ? NV : 1;  // vectors whose modulation is kept
   uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
@@ -438,8 +443,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
   if (threadIdx.x < 32) {
     // the vectors before the rows: behind all CTAs' first rows they would take 4 us
     if (threadIdx.x == 0 && NC == NV && b >= 0) fetch_vectors();
-    __syncwarp();
-    if (static_cast<int>(threadIdx.x) < a.stages && r0 + threadIdx.x < r1) fetch(r0 + threadIdx.x, threadIdx.x);
+    for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
   }
   const int64_t nkb = a.cols >> 4;
   if (a.q_codes != nullptr && blockIdx.x == gridDim.x - 1) {  // block scales of the rows that pad to 128 are 0
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
     const uint8_t* buf = norm_rows + stage * stage_bytes;
     bool freed = false;  // a barrier has been passed since the row's values were read
     auto refill = [&]() {
-      if (!freed && threadIdx.x == 0 && row + a.stages < r1) fetch(row + a.stages, stage);
+      if (!freed && threadIdx.x < 32 && row + a.stages < r1) fetch(row + a.stages, stage);
       freed = true;
     };
     if (b >= 0) {
@@ -783,7 +787,7 @@ __device__ __forceinline__ void cta_sums(float (&s)[6], float* red) {
 
 // A CTA walks the rows of its piece; thread t holds the eight columns at 8 t (and with NV > 1 those
 // at 8 (t + i threads)). Rows come through a ring of row buffers, filled by bulk copies (one per
-// tensor and row, issued by one thread `stages` rows ahead), so the loads of the coming rows are in
+// tensor and row, issued by one warp `stages` rows ahead), so the loads of the coming rows are in
 // flight while a row is reduced. The one barrier of a row's reduction is also what frees its buffer:
 // every thread has read its values by then.
 // POST: the branch has its norm (six row sums, else two). With NV = 1 the sequence's constants per
@@ -806,17 +810,29 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   const uint32_t at_y = at_dh + (has_dh ? half_bytes : 0u), at_stats = at_y + (has_y ? half_bytes : 0u);
   const uint32_t stage_bytes = at_stats + 16u;
 
-  auto fetch = [&](int64_t row, int stage) {  // one thread
-    uint8_t* to = norm_rows + stage * stage_bytes;
-    uint64_t* bar = &full[stage];
-    mbar_arrive_expect_tx(bar, stage_bytes);
-    if (has_dh) {
-      bulk_load(to, static_cast<const ST*>(a.x) + row * a.ldx, stream_bytes, bar);
-      bulk_load(to + at_dh, a.dh + row * a.lddh, half_bytes, bar);
-    }
-    if (has_dxo) bulk_load(to + at_dxo, static_cast<const ST*>(a.dxo) + row * a.lddxo, stream_bytes, bar);
-    if (has_y) bulk_load(to + at_y, a.y + row * a.ldy, half_bytes, bar);
-    bulk_load(to + at_stats, a.stats + 4 * row, 16u, bar);
+  // warp 0 fetches a row, one lane per tensor
+  const int lane = threadIdx.x & 31;
+  const void* const src_of[5] = {a.x, a.dh, a.dxo, a.y, a.stats};
+  const int64_t pitch_of[5] = {a.ldx * static_cast<int64_t>(sizeof(ST)), a.lddh * 2,
+                               a.lddxo * static_cast<int64_t>(sizeof(ST)), a.ldy * 2, 16};
+  const uint32_t bytes_of[5] = {has_dh ? stream_bytes : 0u, has_dh ? half_bytes : 0u, has_dxo ? stream_bytes : 0u,
+                                has_y ? half_bytes : 0u, 16u};
+  const uint32_t at_of[5] = {0u, at_dh, at_dxo, at_y, at_stats};
+  const uint8_t* src = nullptr;
+  int64_t src_pitch = 0;
+  uint32_t src_bytes = 0u, src_at = 0u;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    if (lane != i) continue;
+    src = static_cast<const uint8_t*>(src_of[i]);
+    src_pitch = pitch_of[i];
+    src_bytes = bytes_of[i];
+    src_at = at_of[i];
+  }
+  auto fetch = [&](int64_t row, int stage) {  // warp 0
+    if (lane == 0) mbar_arrive_expect_tx(&full[stage], stage_bytes);
+    __syncwarp();
+    if (src_bytes != 0u) bulk_load(norm_rows + stage * stage_bytes + src_at, src + row * src_pitch, src_bytes, &full[stage]);
   };
   uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
   const NormVectors vecs(a.gate, a.scale, nullptr, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
@@ -838,8 +854,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
   if (threadIdx.x < 32) {
     // the vectors before the rows: behind all CTAs' first rows they would take 4 us
     if (threadIdx.x == 0 && NV == 1 && b >= 0) fetch_vectors();
-    __syncwarp();
-    if (static_cast<int>(threadIdx.x) < a.stages && r0 + threadIdx.x < r1) fetch(r0 + threadIdx.x, threadIdx.x);
+    for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
   }
   __syncthreads();
 
@@ -1040,7 +1055,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kern
       }
     }
     // every thread has passed this row's barrier, so its buffer takes the next row
-    if (threadIdx.x == 0 && row + a.stages < r1) fetch(row + a.stages, stage);
+    if (threadIdx.x < 32 && row + a.stages < r1) fetch(row + a.stages, stage);
     if (++stage == a.stages) {
       stage = 0;
       phase ^= 1u;
