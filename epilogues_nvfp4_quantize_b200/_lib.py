@@ -590,7 +590,7 @@ class ResidualNorm(torch.autograd.Function):
             return (None,) * 12
         dx_out = None if dx_out is None else _rows_of_16_bytes(dx_out)
         dh = None if dh is None else _rows_of_16_bytes(dh)
-        need = ctx.needs_input_grad
+        need = ctx.needs_input_grad + (False,) * 12  # arguments that were left out need none
         make = torch.empty_like if offsets is None else torch.zeros_like
 
         def like(i, t):
