@@ -793,7 +793,7 @@ __device__ __forceinline__ void cta_sums(float (&s)[6], float* red) {
 // POST: the branch has its norm (six row sums, else two). With NV = 1 the sequence's constants per
 // column stay in registers, else they are read again for each row (from L1).
 template <class ST, int NV, bool POST>
-__global__ void __launch_bounds__(normcfg::GRAD_THREADS) residual_norm_grad_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_kernel(const NormGradArgs a) {
   using namespace normcfg;
   extern __shared__ __align__(128) uint8_t norm_rows[];
   __shared__ float red[2][32 * 8];
