@@ -47,7 +47,7 @@ struct DeviceInfo {
   int gemv_clusters[4] = {};
   bool gemv_attr_set[2] = {};
   int norm_regs[8] = {};             // registers of residual_norm_ring_kernel, by stream type, NV and POST
-  bool norm_grad_attr_set[12] = {};  // residual_norm_grad_kernel, by stream type, NV and POST
+  bool norm_grad_attr_set[8] = {};   // residual_norm_grad_kernel, by stream type, POST and CLUSTER
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mutex;
@@ -849,18 +849,21 @@ int64_t out_size(int dtype) { return dtype == NVFP4_OUT_F32 ? 4 : 2; }
 // in a run of them the launch of each overlaps the end of the one before.
 template <class Args>
 nvfp4_status launch_dependent(void (*kern)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                              const Args& args) {
+                              const Args& args, int cluster = 1) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, args) != cudaSuccess) {
     (void)cudaGetLastError();
     return NVFP4_ERR_CUDA;
@@ -1093,60 +1096,58 @@ nvfp4_status launch_norm(DeviceInfo* info, const nvfp4::NormArgs& a, int64_t row
                           static_cast<int>((vecs + 63) / 64 * 32), 0, stream, a);
 }
 
-// Eight-column vectors per thread of the gradient kernel, its threads, and how many of its CTAs
-// share an SM (by registers).
-void norm_grad_shape(int64_t cols, int* nv, int* threads, int* per_sm) {
+// How the gradient kernel takes a row: CTAs that share its columns (4096 each at most), the columns and
+// threads of each, and how many of them share an SM (by registers).
+void norm_grad_shape(int64_t cols, int* cluster, int* cta_cols, int* threads, int* per_sm) {
   const int64_t vecs = cols / 8;
-  *nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
-  *threads = static_cast<int>((vecs + 32 * *nv - 1) / (32 * *nv) * 32);
+  *cluster = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+  const int64_t each = (vecs + *cluster - 1) / *cluster;
+  *cta_cols = static_cast<int>(each * 8);
+  *threads = static_cast<int>((each + 31) / 32 * 32);
   *per_sm = nvfp4::normcfg::GRAD_THREADS / *threads;
 }
 
-// Pieces that the rows are cut into for the gradient: one per CTA that fits on a B200's 148 SMs.
+// Pieces that the rows are cut into for the gradient: one per CTA or cluster that fits on a B200's 148
+// SMs (clusters of 4 do not fill all of its groups of SMs: 32 of 37).
 int64_t norm_chunks(int64_t rows, int64_t cols) {
-  int nv, threads, per_sm;
-  norm_grad_shape(cols, &nv, &threads, &per_sm);
-  const int64_t n = 148ll * per_sm;
+  int cluster, cta_cols, threads, per_sm;
+  norm_grad_shape(cols, &cluster, &cta_cols, &threads, &per_sm);
+  const int64_t n = cluster == 1 ? 148ll * per_sm : cluster == 2 ? 74ll : 32ll;
   return rows < n ? rows : n;
 }
 
-template <class ST, int NV, bool POST>
+template <class ST, bool POST, bool CLUSTER>
 nvfp4_status launch_norm_grad(DeviceInfo* info, nvfp4::NormGradArgs a, cudaStream_t stream) {
   using namespace nvfp4::normcfg;
-  auto kern = nvfp4::residual_norm_grad_kernel<ST, NV, POST>;
+  auto kern = nvfp4::residual_norm_grad_kernel<ST, POST, CLUSTER>;
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    bool& set = info->norm_grad_attr_set[(sizeof(ST) == 4) + 2 * (NV / 2) + 6 * POST];
+    bool& set = info->norm_grad_attr_set[(sizeof(ST) == 4) + 2 * POST + 4 * CLUSTER];
     if (!set) {
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
         return NVFP4_ERR_CUDA;
       set = true;
     }
   }
-  int nv, threads, per_sm;
-  norm_grad_shape(a.cols, &nv, &threads, &per_sm);
-  const int64_t stage = nvfp4::norm_grad_stage(a.cols, sizeof(ST), a.dxo != nullptr, a.dh != nullptr, a.y != nullptr);
-  const int64_t vectors =
-      nv == 1 ? nvfp4::norm_vector_bytes(a.cols, a.mod_f32, (a.gate != nullptr) + (a.scale != nullptr),
-                                         (a.w_post != nullptr) + (a.w != nullptr))
-              : 0;
-  int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // the largest size leaves room for one
+  int threads, per_sm;
+  norm_grad_shape(a.cols, &a.cluster, &a.cta_cols, &threads, &per_sm);
+  const int64_t stage = nvfp4::norm_grad_stage(a.cta_cols, sizeof(ST), a.dxo != nullptr, a.dh != nullptr, a.y != nullptr);
+  const int64_t vectors = nvfp4::norm_vector_bytes(a.cta_cols, a.mod_f32, (a.gate != nullptr) + (a.scale != nullptr),
+                                                   (a.w_post != nullptr) + (a.w != nullptr));
+  int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // the largest size leaves room for three
   const int64_t most = (a.rows + a.chunks - 1) / a.chunks;
   if (stages > GRAD_MAX_STAGES) stages = GRAD_MAX_STAGES;
   if (stages > most) stages = most;
   if (stages < 1) stages = 1;
   a.stages = static_cast<int>(stages);
-  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks)), threads,
-                          static_cast<size_t>(stages * stage + vectors), stream, a);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(a.chunks * a.cluster)), threads,
+                          static_cast<size_t>(stages * stage + vectors), stream, a, a.cluster);
 }
 
 template <class ST, bool POST>
 nvfp4_status launch_norm_grad(DeviceInfo* info, const nvfp4::NormGradArgs& a, cudaStream_t stream) {
-  int nv, threads, per_sm;
-  norm_grad_shape(a.cols, &nv, &threads, &per_sm);
-  return nv == 1   ? launch_norm_grad<ST, 1, POST>(info, a, stream)
-         : nv == 2 ? launch_norm_grad<ST, 2, POST>(info, a, stream)
-                   : launch_norm_grad<ST, 4, POST>(info, a, stream);
+  return a.cols <= 4096 ? launch_norm_grad<ST, POST, false>(info, a, stream)
+                        : launch_norm_grad<ST, POST, true>(info, a, stream);
 }
 
 }  // namespace

@@ -728,6 +728,7 @@ struct NormGradArgs {
   float* dw;              // cols, or null
   float* dw_post;
   int chunks, stages;     // pieces of the rows, row buffers
+  int cluster, cta_cols;  // CTAs that share a row, and the columns of each
   int64_t chunk_rows;     // rows of a piece, and how many pieces have one more
   int chunk_extra;
   float* seq_part;        // (chunks + batches) x 3 x cols, or null (no sums)
@@ -747,13 +748,17 @@ __host__ __device__ constexpr int64_t norm_grad_stage(int64_t cols, int elem, bo
   return cols * (elem * (dxo + dh) + 2 * (dh + y)) + 16;
 }
 
-// Sums over the CTA of the first N of six values per thread (N = 2 or 6); every thread gets them.
-// Within a warp, each of the first log2 exchanges halves the values a lane keeps (9 shuffles for
-// six sums instead of 30); lane 4 k then holds sum k. `red` holds 32 x 8 floats.
-template <int N>
-__device__ __forceinline__ void cta_sums(float (&s)[6], float* red) {
+// Sums over the CTA, or over a cluster that shares the row's columns, of the first N of six values per
+// thread (N = 2 or 6); every thread gets them. Within a warp, each of the first log2 exchanges halves
+// the values a lane keeps (9 shuffles for six sums instead of 30); lane 4 k then holds sum k. `red` holds
+// 32 x 8 floats; in a cluster each warp writes its sums to that place in every CTA, and the cluster's
+// barrier takes the place of the CTA's.
+template <int N, bool CLUSTER>
+__device__ __forceinline__ void row_sums(float (&s)[6], float* red, int rank, int cluster) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float v;
+  bool holds;
+  int at;
   if constexpr (N == 6) {
     float a4[4], a2[2];
     const bool h16 = (lane & 16) != 0, h8 = (lane & 8) != 0, h4 = (lane & 4) != 0;
@@ -768,44 +773,63 @@ __device__ __forceinline__ void cta_sums(float (&s)[6], float* red) {
     v = (h4 ? a2[1] : a2[0]) + __shfl_xor_sync(0xffffffffu, h4 ? a2[0] : a2[1], 4);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
     v += __shfl_xor_sync(0xffffffffu, v, 1);
-    if ((lane & 3) == 0) red[warp * 8 + (lane >> 2)] = v;
+    holds = (lane & 3) == 0;
+    at = lane >> 2;
   } else {
     const bool h16 = (lane & 16) != 0;
     v = (h16 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, h16 ? s[0] : s[1], 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((lane & 15) == 0) red[warp * 8 + (lane >> 4)] = v;
+    holds = (lane & 15) == 0;
+    at = lane >> 4;
   }
-  __syncthreads();
+  int entries = warps;
+  if constexpr (CLUSTER) {
+    entries = cluster * warps;
+    const uint32_t mine = smem_u32(red + (rank * warps + warp) * 8 + at);
+    if (holds) {
+      for (int c = 0; c < cluster; ++c)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(mine, c)), "f"(v) : "memory");
+    }
+    cluster_sync_all();
+  } else {
+    if (holds) red[warp * 8 + at] = v;
+    __syncthreads();
+  }
   v = 0.0f;
-  for (int w = lane >> 3; w < warps; w += 4) v += red[w * 8 + (lane & 7)];
+  for (int w = lane >> 3; w < entries; w += 4) v += red[w * 8 + (lane & 7)];
   v += __shfl_xor_sync(0xffffffffu, v, 8);
   v += __shfl_xor_sync(0xffffffffu, v, 16);
 #pragma unroll
   for (int k = 0; k < N; ++k) s[k] = __shfl_sync(0xffffffffu, v, k);
 }
 
-// A CTA walks the rows of its piece; thread t holds the eight columns at 8 t (and with NV > 1 those
-// at 8 (t + i threads)). Rows come through a ring of row buffers, filled by bulk copies (one per
-// tensor and row, issued by one warp `stages` rows ahead), so the loads of the coming rows are in
-// flight while a row is reduced. The one barrier of a row's reduction is also what frees its buffer:
-// every thread has read its values by then.
-// POST: the branch has its norm (six row sums, else two). With NV = 1 the sequence's constants per
-// column stay in registers, else they are read again for each row (from L1).
-template <class ST, int NV, bool POST>
+// A CTA walks the rows of its piece; thread t holds eight columns. Rows come through a ring of row
+// buffers, filled by bulk copies (one per tensor and row, issued by one warp `stages` rows ahead), so the
+// loads of the coming rows are in flight while a row is reduced. The one barrier of a row's reduction is
+// also what frees its buffer: every thread has read its values by then.
+// POST: the branch has its norm (six row sums, else two).
+// CLUSTER: above 4096 columns the CTAs of a cluster of 2 or 4 share a row's columns, so that a thread's
+// sums and the sequence's vectors still fit in its registers (with 16 columns per thread, spilling and
+// reading the vectors again for each row, 8192 x 5120 took 291 us).
+template <class ST, bool POST, bool CLUSTER>
 __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_kernel(const NormGradArgs a) {
   using namespace normcfg;
   extern __shared__ __align__(128) uint8_t norm_rows[];
-  __shared__ float red[2][32 * 8];
+  __shared__ float red[2][(CLUSTER ? 4 : 1) * 16 * 8];
   __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES], vec_full;
   __shared__ int abort_flag;
   griddep_launch_dependents();
-  const int g = blockIdx.x;
+  constexpr int NV = 1;
+  const int cluster = CLUSTER ? a.cluster : 1;
+  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0, g = static_cast<int>(blockIdx.x) / cluster;
+  const int col0 = rank * a.cta_cols;  // this CTA's columns
+  const int ncols = static_cast<int>(a.cols) - col0 < a.cta_cols ? static_cast<int>(a.cols) - col0 : a.cta_cols;
   const int64_t r0 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g), r1 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g + 1);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   const bool has_dxo = a.dxo != nullptr, has_dh = a.dh != nullptr, has_y = a.y != nullptr;
   // the parts of a row buffer
-  const uint32_t stream_bytes = static_cast<uint32_t>(a.cols * sizeof(ST)), half_bytes = static_cast<uint32_t>(a.cols * 2);
+  const uint32_t stream_bytes = static_cast<uint32_t>(ncols * sizeof(ST)), half_bytes = static_cast<uint32_t>(ncols * 2);
   const uint32_t at_dxo = has_dh ? stream_bytes : 0u, at_dh = at_dxo + (has_dxo ? stream_bytes : 0u);
   const uint32_t at_y = at_dh + (has_dh ? half_bytes : 0u), at_stats = at_y + (has_y ? half_bytes : 0u);
   const uint32_t stage_bytes = at_stats + 16u;
@@ -824,7 +848,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 #pragma unroll
   for (int i = 0; i < 5; ++i) {
     if (lane != i) continue;
-    src = static_cast<const uint8_t*>(src_of[i]);
+    src = static_cast<const uint8_t*>(src_of[i]) + (i == 4 ? 0 : col0 * (i == 0 || i == 2 ? static_cast<int>(sizeof(ST)) : 2));
     src_pitch = pitch_of[i];
     src_bytes = bytes_of[i];
     src_at = at_of[i];
@@ -835,7 +859,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
     if (src_bytes != 0u) bulk_load(norm_rows + stage * stage_bytes + src_at, src + row * src_pitch, src_bytes, &full[stage]);
   };
   uint8_t* const vec_buf = norm_rows + a.stages * stage_bytes;
-  const NormVectors vecs(a.gate, a.scale, nullptr, POST ? a.w_post : nullptr, a.w, a.cols, a.mod_f32);
+  const NormVectors vecs(a.gate, a.scale, nullptr, POST ? a.w_post : nullptr, a.w, ncols, a.mod_f32);
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
@@ -846,73 +870,51 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
   int64_t b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, r0), seq_end = r0;
   auto fetch_vectors = [&]() {  // one thread
     mbar_arrive_expect_tx(&vec_full, vecs.bytes());
-    vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate, a.mod_f32, &vec_full);
-    vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale, a.mod_f32, &vec_full);
-    vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, 0, a.mod_f32, &vec_full);
-    vecs.fetch(NormVectors::W, vec_buf, a.w, 0, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::GATE, vec_buf, a.gate, b * a.ldgate + col0, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::SCALE, vec_buf, a.scale, b * a.ldscale + col0, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::W_POST, vec_buf, a.w_post, col0, a.mod_f32, &vec_full);
+    vecs.fetch(NormVectors::W, vec_buf, a.w, col0, a.mod_f32, &vec_full);
   };
   if (threadIdx.x < 32) {
     // the vectors before the rows: behind all CTAs' first rows they would take 4 us
-    if (threadIdx.x == 0 && NV == 1 && b >= 0) fetch_vectors();
+    if (threadIdx.x == 0 && b >= 0) fetch_vectors();
     for (int i = 0; i < a.stages && r0 + i < r1; ++i) fetch(r0 + i, i);
   }
   __syncthreads();
+  if constexpr (CLUSTER) cluster_sync_all();  // every CTA of the cluster has started
 
   bool live[NV];
   int col[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     col[i] = 8 * static_cast<int>(threadIdx.x + i * blockDim.x);
-    live[i] = col[i] < a.cols;
+    live[i] = col[i] < ncols;
   }
   float s_dh[NV][8], s_dhx[NV][8], s_ty[NV][8];  // sums over the current sequence's rows
-  constexpr int NC = NV == 1 ? 1 : 0;
-  float c_w[NC + 1][8], c_g[NC + 1][8], c_a[NC + 1][8];  // w (1 + scale), the gate, gate w_post
+  float c_w[NV][8], c_g[NV][8], c_a[NV][8];  // w (1 + scale), the gate, gate w_post
   bool first_flush = true, seq_begins = false;
 
-  // the sequence's constants of vector i, from global memory
-  auto constants = [&](int i, float (&cw)[8], float (&gt)[8], float (&ag)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) cw[k] = gt[k] = 1.0f;
-    if (a.scale != nullptr) {
-      load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], cw);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) cw[k] += 1.0f;
-    }
-    if (a.w != nullptr) {
-      load8_f32(a.w + col[i], ag);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) cw[k] *= ag[k];
-    }
-    if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], gt);
-    if constexpr (POST) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ag[k] = 1.0f;
-      if (a.w_post != nullptr) load8_f32(a.w_post + col[i], ag);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ag[k] *= gt[k];
-    }
-  };
   auto flush = [&](int64_t next_row) {
     if (a.seq_part == nullptr) return;  // no sums are asked for
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && rank == 0) {
       if (seq_begins) a.seq_pieces[2 * b] = g;
       if (next_row >= seq_end || next_row >= a.rows) a.seq_pieces[2 * b + 1] = g;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!live[i]) continue;
-      float* p = a.seq_part + (g + b) * 3 * a.cols + col[i];
+      const int at = col0 + col[i];
+      float* p = a.seq_part + (g + b) * 3 * a.cols + at;
       store8_f32(p, s_dh[i]);
       store8_f32(p + a.cols, s_dhx[i]);
       store8_f32(p + 2 * a.cols, s_ty[i]);
       if (a.w_part != nullptr) {
-        float* q = a.w_part + static_cast<int64_t>(g) * 2 * a.cols + col[i];
+        float* q = a.w_part + static_cast<int64_t>(g) * 2 * a.cols + at;
         float w0[8], p0[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w0[k] = 0.0f, p0[k] = 1.0f;
-        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + col[i], w0);
-        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + col[i], p0);
+        if (a.scale != nullptr) load8_mod(a.scale, a.mod_f32, b * a.ldscale + at, w0);
+        if (a.gate != nullptr) load8_mod(a.gate, a.mod_f32, b * a.ldgate + at, p0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           w0[k] = (1.0f + w0[k]) * s_dhx[i][k];
@@ -954,7 +956,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 #pragma unroll
           for (int k = 0; k < 8; ++k) s_dh[i][k] = s_dhx[i][k] = s_ty[i][k] = 0.0f;
         }
-        if constexpr (NV == 1) {
+        {
           // a barrier lies behind since the last sequence's were read
           if (threadIdx.x == 0 && row != r0) fetch_vectors();
           (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 83);
@@ -976,7 +978,11 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
     (void)mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 80);
     const uint8_t* buf = norm_rows + stage * stage_bytes;
     if (skip) {
-      __syncthreads();
+      if constexpr (CLUSTER) {
+        cluster_sync_all();
+      } else {
+        __syncthreads();
+      }
     } else {
       const float4 st = *reinterpret_cast<const float4*>(buf + at_stats);
       const float mean = st.x, rstd = st.y, rstd_y = POST ? st.z : 1.0f;
@@ -987,7 +993,6 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 #pragma unroll
         for (int k = 0; k < 8; ++k) xh[i][k] = d[i][k] = t[i][k] = yh[i][k] = 0.0f;
         if (!live[i]) continue;
-        if constexpr (NV > 1) constants(i, c_w[0], c_g[0], c_a[0]);
         Stream8<ST> v;
         if (has_dxo) {
           v.load(buf + at_dxo, col[i]);
@@ -1025,13 +1030,12 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
           }
         }
       }
-      cta_sums<POST ? 6 : 2>(s, red[static_cast<int>(row - r0) & 1]);
+      row_sums<POST ? 6 : 2, CLUSTER>(s, red[static_cast<int>(row - r0) & 1], rank, cluster);
       const float m1 = a.norm == NORM_LAYER ? s[0] * inv_n : 0.0f, m2 = s[1] * inv_n;
       const float m3 = POST ? (s[2] + rstd * (s[3] - m1 * s[4] - m2 * s[5])) * inv_n : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!live[i]) continue;
-        if constexpr (NV > 1) constants(i, c_w[0], c_g[0], c_a[0]);
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -1042,7 +1046,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
         if (a.dx != nullptr) {
           Stream8<ST> v;
           v.round(o);
-          v.store(a.dx, row * a.lddx + col[i]);
+          v.store(a.dx, row * a.lddx + col0 + col[i]);
         }
         if (a.dy != nullptr) {
 #pragma unroll
@@ -1050,7 +1054,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
             o[k] = POST ? rstd_y * (c_a[0][k] * t[i][k] - yh[i][k] * m3) : c_g[0][k] * t[i][k];
           Stream8<uint16_t> v;
           v.round(o);
-          v.store(a.dy, row * a.lddy + col[i]);
+          v.store(a.dy, row * a.lddy + col0 + col[i]);
         }
       }
     }
@@ -1067,11 +1071,12 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
     for (int i = 0; i < NV; ++i) {
       if (!live[i]) continue;
       for (int k = 0; k < 8; ++k) {
-        a.w_part[static_cast<int64_t>(g) * 2 * a.cols + col[i] + k] = 0.0f;
-        a.w_part[(static_cast<int64_t>(g) * 2 + 1) * a.cols + col[i] + k] = 0.0f;
+        a.w_part[static_cast<int64_t>(g) * 2 * a.cols + col0 + col[i] + k] = 0.0f;
+        a.w_part[(static_cast<int64_t>(g) * 2 + 1) * a.cols + col0 + col[i] + k] = 0.0f;
       }
     }
   }
+  if constexpr (CLUSTER) cluster_sync_all();  // no CTA leaves while another may write its sums there
 }
 
 // Adds up the slots of each sequence and the pieces' weight sums. Block (x, y): columns 32 x and
