@@ -372,7 +372,7 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
         stream = torch._C._cuda_getCurrentRawStream(dev)  # current_stream() would build an object: 2 us
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):

@@ -881,10 +881,10 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -896,10 +896,10 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM) != cudaSuccess)
           return NVFP4_ERR_CUDA;
       }
-      cfg.numAttrs = 1;
+      cfg.numAttrs = 2;
       cfg.dynamicSmemBytes = MAX_SMEM;
       for (int i = 0; i < 4; ++i) {
-        attr[0].val.clusterDim.x = 1u << i;
+        attr[1].val.clusterDim.x = 1u << i;
         cfg.gridDim = dim3(static_cast<unsigned>(info->sm_count >> i << i), 1, 1);
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kerns[0], &cfg) != cudaSuccess || n <= 0) return NVFP4_ERR_CUDA;
@@ -943,8 +943,8 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   int n = (a.strips + per_cluster - 1) / per_cluster;
   if (n > clusters[a.cluster_log2]) n = clusters[a.cluster_log2];
   a.strips_at_once = n * per_cluster;
-  attr[0].val.clusterDim.x = 1u << a.cluster_log2;
-  cfg.numAttrs = 2;
+  attr[1].val.clusterDim.x = 1u << a.cluster_log2;
+  cfg.numAttrs = a.cluster_log2 > 0 ? 2 : 1;
   cfg.gridDim = dim3(static_cast<unsigned>(n << a.cluster_log2), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)), 1);
   cfg.dynamicSmemBytes =
       static_cast<size_t>(nvfp4::gemv_smem(NT, depth_i == 0 ? 8 : 4, a.M, a.kslice, 1 << a.cluster_log2));
