@@ -7,8 +7,11 @@
 // and the norm reads the rounded value: the gradient, which only has the stored x', then
 // differentiates exactly what was computed. h is rounded to bf16 once; its NVFP4 form quantises
 // those bf16 values, as every re-quantised output of this library does.
-// Sums, means and reciprocal roots are float32; the variance is taken from centred values (a
-// second pass over registers), so a mean much larger than the spread costs no digits.
+// Sums, means and reciprocal roots are float32; the variance is taken from centred values (about the
+// row's mean, or about each warp's and joined), so a mean much larger than the spread costs no digits.
+//
+// All of it is HBM-bound: forward 2 + 2 + 2 + 2 bytes per value in bf16 (x, y, x', h), gradient 12
+// (x', y, dx', dh, dx, dy).
 #pragma once
 
 #include "ptx.cuh"
@@ -155,8 +158,8 @@ __device__ __forceinline__ void store8_f32(float* p, float (&v)[8]) {
   s.store(p, 0);
 }
 
-// Sum over the threads of a row: one warp (ONE_WARP), or all of the CTA's (red: 32 floats,
-// flipped between two halves by the caller so that one barrier per sum suffices).
+// Sum over the threads of a row: one warp (ONE_WARP), or all of the CTA's (red: 32 floats that no other
+// sum uses, so that one barrier suffices).
 template <bool ONE_WARP>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
@@ -341,7 +344,10 @@ __global__ void __launch_bounds__(ONE_WARP ? 128 : 1024) residual_norm_kernel(co
 
 namespace normcfg {
 constexpr int FWD_MAX_STAGES = 8;
-constexpr int RING_ROWS = 2;             // rows per CTA from which the ring kernel is taken
+// Rows per CTA from which the ring kernel is taken. Ring against one row per CTA, us (bf16): at 2 rows
+// 4096 columns 5.9 / 6.0, 8192 6.0 / 5.2, 1024 6.2 / 6.9; at 2.7 rows 2560 columns 7.4 / 6.0; at 4 rows
+// 4096 columns 10.7 / 13.6, 8192 10.8 / 13.4, 1024 11.8 / 15.5.
+constexpr int RING_ROWS = 3;
 constexpr int SMEM = 220 * 1024;         // per SM, for its CTAs' row buffers and SMEM_OTHER each
 constexpr int SMEM_OTHER = 3584;         // a CTA's static and reserved shared memory
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
@@ -690,7 +696,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
 // mean(a yh) depends on T; it is expanded into sums that do not (six row sums in all), so that a
 // row needs one reduction only.
 //
-// Rows are cut into `chunks` contiguous pieces, one CTA each; a thread keeps its columns and
+// Rows are cut into `chunks` contiguous pieces, one CTA or cluster each; a thread keeps its columns and
 // adds up the three sums in registers over the rows of its piece. Where a sequence ends, the sums
 // go to slot chunk + sequence of the workspace (that index grows with every piece, so no two
 // pieces share one); norm_grad_reduce_kernel adds a sequence's slots in their order. No atomics:

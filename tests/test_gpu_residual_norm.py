@@ -142,17 +142,17 @@ def test_forward(rows, cols, B, opt):
 
 # enough rows that a CTA walks several of them
 MANY_ROWS = [
-    (700, 4096, 2, dict(post=True, w=True, alpha=0.8)),
-    (613, 4096, 1, dict(stream="f32", mod="f32", norm="rms", w=True)),
-    (2501, 1024, 1, dict(branch=False)),
-    (4800, 64, 3, dict(post=True, mod="f32")),
-    (5000, 8, 1, dict(mods=())),
-    (900, 2568, 4, dict(offsets=[0, 1, 1, 700, 890], stream="f32", post=True, w=True, norm="rms")),
-    (1500, 2048, 3, dict(offsets=[3, 900, 1400, 1500], w=True)),
-    (301, 8200, 1, dict(post=True)),
-    (302, 16384, 2, dict(stream="f32", w=True)),
-    (640, 4032, 2, dict(norm=None, post=True, w=True, alpha=0.5)),
-    (640, 3968, 5, dict(norm=None)),
+    (1000, 4096, 2, dict(post=True, w=True, alpha=0.8)),
+    (913, 4096, 1, dict(stream="f32", mod="f32", norm="rms", w=True)),
+    (4201, 1024, 1, dict(branch=False)),
+    (7200, 64, 3, dict(post=True, mod="f32")),
+    (7400, 8, 1, dict(mods=())),
+    (1500, 2568, 4, dict(offsets=[0, 1, 1, 1100, 1490], stream="f32", post=True, w=True, norm="rms")),
+    (2500, 2048, 3, dict(offsets=[3, 900, 2400, 2500], w=True)),
+    (501, 8200, 1, dict(post=True)),
+    (502, 16384, 2, dict(stream="f32", w=True)),
+    (940, 4032, 2, dict(norm=None, post=True, w=True, alpha=0.5)),
+    (940, 3968, 5, dict(norm=None)),
 ]
 
 
