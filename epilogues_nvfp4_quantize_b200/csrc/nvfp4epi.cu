@@ -1401,6 +1401,13 @@ NVFP4_API nvfp4_status rope_axes(const void* x, int dtype, int64_t rows, int64_t
     }
   }
   a.rows_per_cta = static_cast<int>(r);
+  a.units = static_cast<int>(units);
+  a.slots = static_cast<int>(slots);
+  a.step_rows = static_cast<int>(slots / heads);
+  a.step_heads = static_cast<int>(slots % heads);
+  a.inv_units = 1.0f / static_cast<float>(units);
+  a.inv_heads = 1.0f / static_cast<float>(heads);
+  a.inv_pairs = 1.0f / static_cast<float>(n);
   const size_t smem = static_cast<size_t>(r * a.table_pitch) * 2 * sizeof(float);
   const bool inter = interleaved != 0;
   return dtype == NVFP4_OUT_F32   ? launch_rope<float>(a, inter, smem, stream)

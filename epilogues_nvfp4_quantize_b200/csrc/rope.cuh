@@ -45,7 +45,16 @@ struct RopeArgs {
   int rows_per_cta;
   int in_place;                          // y is x: what passes through stays where it is
   int table_pitch;                       // pairs per row of the table (npairs to the next multiple of 4)
+  int units, slots;                      // pieces of a head, and how many heads the CTA takes at once
+  int step_rows, step_heads;             // `slots` heads further on
+  float inv_units, inv_heads, inv_pairs; // for quotients of small numbers
 };
+
+// a / b for 0 <= a < 2^15 and 0 < b < 2^15, with inv_b = 1 / b: the float32 error is below 2^-7 / b, and
+// a + 1/2 keeps the quotient 1 / (2 b) away from the next whole number.
+__device__ __forceinline__ int small_quotient(int a, float inv_b) {
+  return static_cast<int>((static_cast<float>(a) + 0.5f) * inv_b);
+}
 
 template <class T>
 struct RopeVec;  // 16 bytes of T as floats
@@ -107,7 +116,7 @@ __device__ __forceinline__ void rope_put(__half* p, float v) { *p = __float2half
 // time: interleaved with one another, they conflicted in shared memory's banks).
 __device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int nrows, float* cosines, float* sines) {
   for (int i = threadIdx.x; i < nrows * a.npairs; i += ropecfg::THREADS) {
-    const int r = i / a.npairs, p = i - r * a.npairs;
+    const int r = small_quotient(i, a.inv_pairs), p = i - r * a.npairs;
     int ax = 0;
 #pragma unroll
     for (int k = 0; k < ropecfg::MAX_AXES - 1; ++k) ax += p >= a.axis_end[k] ? 1 : 0;
@@ -140,22 +149,27 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   griddep_launch_dependents();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_cta;
   const int nrows = static_cast<int>(a.rows - row0 < a.rows_per_cta ? a.rows - row0 : a.rows_per_cta);
-  const int n = a.npairs;
-  const int units = MODE == ROPE_INTERLEAVED ? a.head_dim / V
-                    : MODE == ROPE_HALVES    ? n / V + (a.head_dim - 2 * n) / V
-                                             : a.head_dim - n;
-  const int slots = units < THREADS ? THREADS / units : 1;
-  const int slot = units < THREADS ? threadIdx.x / units : 0;
+  const int n = a.npairs, units = a.units, slots = a.slots;
+  const int slot = slots > 1 ? small_quotient(threadIdx.x, a.inv_units) : 0;
   const int total = nrows * a.heads;
-  // (row, head) of this thread's j-th step, advanced without divisions
-  const int dr = slots / a.heads, dh = slots - dr * a.heads;
-  const int r_first = slot / a.heads, h_first = slot - r_first * a.heads;
-  auto advance = [&](int& r, int& h) {
-    r += dr;
-    h += dh;
-    if (h >= a.heads) {
-      h -= a.heads;
-      ++r;
+  // Row and head of this thread's first step, then `slots` heads further each time; offsets are moved
+  // along instead of multiplied out.
+  const int r_first = small_quotient(slot, a.inv_heads), h_first = slot - r_first * a.heads;
+  struct Place {
+    int r, h;
+    int64_t at;  // element of x or y
+  };
+  auto first = [&](int64_t row, int64_t head) { return Place{r_first, h_first, r_first * row + h_first * head}; };
+  const int64_t x_step = a.step_rows * a.x_row + a.step_heads * a.x_head, x_wrap = a.x_row - a.heads * a.x_head;
+  const int64_t y_step = a.step_rows * a.y_row + a.step_heads * a.y_head, y_wrap = a.y_row - a.heads * a.y_head;
+  auto advance = [&](Place& p, int64_t step, int64_t wrap) {
+    p.r += a.step_rows;
+    p.h += a.step_heads;
+    p.at += step;
+    if (p.h >= a.heads) {
+      p.h -= a.heads;
+      ++p.r;
+      p.at += wrap;
     }
   };
   const T* const x = static_cast<const T*>(a.x) + row0 * a.x_row;
@@ -172,19 +186,20 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
   unit();
   const bool works = slot < slots && u < units;
   uint4 lo[B], hi[B];
-  auto load = [&](int j, int r, int h) {
+  Place from = first(a.x_row, a.x_head);
+  auto load = [&](int j) {
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       if (j + k * slots < total) {
-        const T* src = x + r * a.x_row + h * a.x_head + e0;
+        const T* src = x + from.at + e0;
         lo[k] = *reinterpret_cast<const uint4*>(src);
         if (MODE == ROPE_HALVES && rotates) hi[k] = *reinterpret_cast<const uint4*>(src + n);
       }
-      advance(r, h);
+      advance(from, x_step, x_wrap);
     }
   };
   griddep_wait();  // nothing before this reads or writes global memory
-  if (MODE != ROPE_HALVES_SCALAR && works && (rotates || !a.in_place)) load(slot, r_first, h_first);
+  if (MODE != ROPE_HALVES_SCALAR && works && (rotates || !a.in_place)) load(slot);
   rope_table(a, row0, nrows, rope_cos, rope_sin);
   __syncthreads();
   if (!works) return;
@@ -195,17 +210,20 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
     // the pairs' cos and sin stay in registers while the row is the same
     float c[NP], sn[NP];
     const bool whole = (u + 1) * NP <= n;  // else the unit's last pairs pass through
-    int r = r_first, h = h_first, of = -1;
+    Place to = first(a.y_row, a.y_head);
+    int of = -1;
+    if (u >= THREADS || MODE == ROPE_HALVES_SCALAR) from = first(a.x_row, a.x_head);
     for (int j = slot; j < total; j += B * slots) {
       if constexpr (MODE != ROPE_HALVES_SCALAR) {
-        if (j != slot || u >= THREADS) load(j, r, h);
+        if (j != slot || u >= THREADS) load(j);
       }
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         if (j + k * slots < total) {
-          T* const dst = y + r * a.y_row + h * a.y_head + e0;
+          T* const dst = y + to.at + e0;
+          const int r = to.r;
           if constexpr (MODE == ROPE_HALVES_SCALAR) {
-            const T* const src = x + r * a.x_row + h * a.x_head + e0;
+            const T* const src = x + from.at + e0;
             if (!rotates) {
               *dst = *src;
             } else {
@@ -265,7 +283,8 @@ __global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a
             *reinterpret_cast<uint4*>(dst) = lo[k];
           }
         }
-        advance(r, h);
+        advance(to, y_step, y_wrap);
+        if constexpr (MODE == ROPE_HALVES_SCALAR) advance(from, x_step, x_wrap);
       }
     }
   }
