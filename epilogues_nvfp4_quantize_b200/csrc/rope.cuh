@@ -138,7 +138,7 @@ __device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t row0, int 
 // Threads keep their unit and walk the (row, head) pairs of the CTA, a batch at a time. A CTA's first
 // batch is loaded before its table is made, so the positions, the angles and x travel together.
 template <class T, int MODE>
-__global__ void __launch_bounds__(ropecfg::THREADS) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(ropecfg::THREADS, MODE == ROPE_HALVES ? 3 : 4) rope_kernel(const RopeArgs a) {
   using namespace ropecfg;
   using RV = RopeVec<T>;
   constexpr int V = RV::V;
