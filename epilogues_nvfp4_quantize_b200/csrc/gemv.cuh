@@ -9,11 +9,10 @@
 // and up to 8 rows of x per instruction: with so few rows tcgen05 would need the weights decoded
 // into shared memory first, while here they go from a 16-byte global load through registers into
 // the instruction. A weight's value without G, level x block scale, has at most 6 significant bits
-// between 2^-10 and 2688 and is exact in f16. x goes to f16 by a power of two per row (the largest
-// finite magnitude of the row's slice goes to [2^14, 2^15)): every bf16 value down to 2^-28 of the
-// largest stays exact and smaller ones are off by at most 2^-39 of it, below float32's own sums;
-// infinities and NaN stay what they are. So the arithmetic is that of float32 sums of exact
-// products.
+// between 2^-10 and 2688 and is exact in f16. x goes to f16 by a power of two for each 128 columns of a
+// row (their largest finite magnitude goes to [2^14, 2^15)): every bf16 value down to 2^-28 of that
+// stays exact and smaller ones are off by at most 2^-39 of it, below float32's own sums; infinities and
+// NaN stay what they are. So the arithmetic is that of float32 sums of exact products.
 //
 // A strip is 16 weight rows: rows r .. r+3 of each of the four 32-row quarters of a 128-row scale
 // tile. In the tensor-core scale layout the four quarters' scales of a row are adjacent, so a strip
@@ -26,7 +25,6 @@
 #include "ptx.cuh"
 #include "codec.cuh"
 #include "quantize.cuh"
-#include "unfused.cuh"
 
 namespace nvfp4 {
 
@@ -67,7 +65,7 @@ __host__ __device__ constexpr int gemv_x_pitch(int kslice) { return kslice * 2 +
 __host__ __device__ constexpr int gemv_smem(int nt, int depth, int64_t tokens, int kslice, int cluster) {
   return gemvcfg::WARPS * depth * gemvcfg::SLOT +                                                // ring of weights
          2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? gemvcfg::ROUND * 512 * nt : 0) +         // joins
-         8 * nt * 8 +                                                                            // row factors
+         kslice / gemvcfg::GROUP * 8 * nt * 4 +                                                  // factors of x
          static_cast<int>(tokens < 8 * nt ? tokens : 8 * nt) * gemv_x_pitch(kslice);             // x
 }
 
@@ -84,6 +82,32 @@ __device__ __forceinline__ void gemv_unpack(const uint4& q, int f16, float (&f)[
       f[2 * i + 1] = bf16_hi(w[i]);
     }
   }
+}
+
+// x / (1 + e^-x) in five instructions (about 2^-22 of the value, growing with |x| as the rounding of
+// x log2(e) does; it is rounded to 16 bits next).
+__device__ __forceinline__ float gemv_silu(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(-1.4426950408889634f * x)));
+  return x * r;
+}
+
+// Largest finite magnitude of eight 16-bit floats: without their signs they compare like integers, two
+// at a time; where infinities or NaN come out on top, they are left out one by one.
+__device__ __forceinline__ float gemv_finite_amax(const uint4& q, int f16) {
+  const uint32_t w[4] = {q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu, q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu};
+  const uint32_t m2 = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+  const uint32_t inf = f16 ? 0x7C00u : 0x7F80u;
+  if (m >= inf) {
+    m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
+      m = max(m, max(lo < inf ? lo : 0u, hi < inf ? hi : 0u));
+    }
+  }
+  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(m))) : __uint_as_float(m << 16);
 }
 
 // Eight E2M1 codes to four f16 pairs, in their order. Taking the bytes apart inside the PTX costs
@@ -157,9 +181,8 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
   uint8_t* ring = gemv_smem_raw;                                               // [WARPS][DEPTH][SLOT]
   float* red = reinterpret_cast<float*>(ring + WARPS * DEPTH * SLOT);          // [2][WARPS][32][4 NT]
   float* part = red + 2 * WARPS * 128 * NT;                                    // [ROUND][32][4 NT] (clusters)
-  float* inv = part + (cluster > 1 ? ROUND * 128 * NT : 0);                    // factor of each row of x
-  unsigned* amax = reinterpret_cast<unsigned*>(inv + 8 * NT);
-  uint8_t* xs = reinterpret_cast<uint8_t*>(amax + 8 * NT);                     // [tokens][pitch]
+  float* inv = part + (cluster > 1 ? ROUND * 128 * NT : 0);                    // [groups][8 NT] factors of x
+  uint8_t* xs = reinterpret_cast<uint8_t*>(inv + a.kslice / GROUP * 8 * NT);   // [tokens][pitch]
 
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -173,7 +196,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
 
   // ---- this slice of x on its way into shared memory -------------------------------------
   // Columns 32 t + 8 w .. + 7 of a group sit at 64 w + 16 t bytes of it. Each row is taken by as
-  // many warps as there are (one at least); a thread comes back to the same vectors in each pass.
+  // many warps as there are (one at least); a half-warp takes a whole group.
   const int vecs = klen >> 3, xvecs = a.kslice >> 3;
   const int xwarps_log2 = tokens <= 1 ? 4 : tokens <= 2 ? 3 : tokens <= 4 ? 2 : tokens <= 8 ? 1 : 0;
   const int xm = warp >> xwarps_log2;
@@ -189,7 +212,6 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     each_vector([&](int v, uint4* p) { copy_async16(smem_u32(p), v < vecs ? row + 8 * v : a.x, v < vecs ? 16 : 0); });
   }
   copy_async_commit();
-  if (tid < 8 * NT) amax[tid] = 0u;
   const float G = *a.gscale;
 
   // ---- the walk over weights: step = one 128-column group of one strip ---------------------
@@ -250,54 +272,40 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
 #pragma unroll
   for (int j = 0; j < FIRST; ++j) load(my_ring + j * SLOT);
 
-  // ---- x to f16, each row by its power of two ---------------------------------------------
+  // ---- x to f16, each 128 columns of a row by their power of two -------------------------
+  // The largest finite magnitude of a group goes to [2^14, 2^15). A half-warp holds the group, so
+  // nothing has to be known of the rest of the row, and the products of a group are scaled back when
+  // they are added to the others.
   copy_async_wait<FIRST>();
   if (a.x_f16 && !a.silu) {  // f16 needs no factor
-    if (tid < 8 * NT) inv[tid] = 1.0f;
+    for (int i = tid; i < a.kslice / GROUP * 8 * NT; i += THREADS) inv[i] = 1.0f;
   } else {
-    __syncthreads();  // amax is 0
-    // Pass 1: f(x) as it is stored (16 bits), and the largest finite magnitude of each row.
-    float big = 0.0f;
     each_vector([&](int v, uint4* p) {
       uint4 q = *p;
-      if (a.silu) {
-        float f[8];
+      float f[8];
+      if (a.silu) {  // rounded to x's type
         gemv_unpack(q, a.x_f16, f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = silu_f32(f[k]);
+        for (int k = 0; k < 8; ++k) f[k] = gemv_silu(f[k]);
         q = a.x_f16 ? make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
                                  pack_f16x2(f[6], f[7]))
                     : make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                                  pack_bf16x2(f[6], f[7]));
-        *p = q;
       }
-      float f[8];
       gemv_unpack(q, a.x_f16, f);
+      float big = gemv_finite_amax(q, a.x_f16);
+      const uint32_t half = 0xFFFFu << (lane & 16);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float z = fabsf(f[k]);
-        big = fmaxf(big, z <= 3.4028234663852886e38f ? z : 0.0f);
-      }
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-    if (lane == 0 && xm < tokens) atomicMax(amax + xm, __float_as_uint(big));
-    __syncthreads();
-    // Pass 2: to f16, by the row's factor 2^(14 - e); the clamp keeps it and its inverse normal
-    // float32 numbers.
-    if (xm < tokens) {
-      int e = static_cast<int>(amax[xm] >> 23) - 127;
+      for (int o = 8; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(half, big, o));
+      // 2^(14 - e) and its inverse; the clamp keeps both normal float32 numbers
+      int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
       if (e < -100) e = -100;
       const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-      if (lane == 0) inv[xm] = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
-      each_vector([&](int, uint4* p) {
-        float f[8];
-        gemv_unpack(*p, a.x_f16, f);
+      if ((lane & 15) == 0) inv[(v >> 4) * 8 * NT + xm] = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= up;
-        *p = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
-      });
-    }
+      for (int k = 0; k < 8; ++k) f[k] *= up;
+      *p = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+    });
   }
 #pragma unroll
   for (int j = FIRST; j < DEPTH; ++j) load(my_ring + j * SLOT);
@@ -350,10 +358,13 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
         mma_16x8x16(one[n], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
       }
     }
+    const float* const factor = inv + (gb + step) * 8 * NT + 2 * t;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      const float2 f = *reinterpret_cast<const float2*>(factor + 8 * n);  // of rows 2 t and 2 t + 1
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] += one[n][i];
+      for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(one[n][i], i & 1 ? f.y : f.x, acc[n][i]);
+    }
   };
   // Value i of lane's fragment: weight row g or g + 8 of the strip, row 2 t or 2 t + 1 of x
   float bias[2] = {0.0f, 0.0f};
@@ -419,10 +430,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     }
     if (mine) {
 #pragma unroll
-      for (int i = 0; i < 4 * NT; ++i) {
-        const int m = 8 * (i >> 2) + 2 * t + (i & 1);
-        sum[i] = sum[i] * G * (m < tokens ? inv[m] : 0.0f);
-      }
+      for (int i = 0; i < 4 * NT; ++i) sum[i] *= G;
       if (cluster == 1) {
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i) put(strip, i >> 2, i & 3, sum[i]);

@@ -301,9 +301,9 @@ nvfp4_status swiglu_bf16(const void* c, int64_t rows, int64_t nh, int64_t ldc,
  *   act: NVFP4_ACT_NONE (f the identity) or NVFP4_ACT_SILU (f(x) = x / (1 + exp(-x)), rounded to
  *        x's type as a separate kernel would leave it).
  *   bias: N float32, or NULL.  D: M x N of out_dtype, leading dimension ldd elements.
- * Products are exact and sums float32; x is held in f16 scaled by a power of two per row, which is
- * exact for every value down to 2^-28 of the row's largest finite one and off by at most 2^-39 of
- * that below. Infinities and NaN in x reach the outputs of their row only.
+ * Products are exact and sums float32; x is held in f16, scaled by a power of two for each 128 columns
+ * of a row, which is exact for every value down to 2^-28 of their largest finite one and off by at most
+ * 2^-39 of that below. Infinities and NaN in x reach the outputs of their row only.
  * Rules: M >= 1 (rows are taken 16 at a time: past 16, the weight is read again for each 16 rows),
  *        N >= 1, K % 64 == 0, K <= 32768 (UNSUPPORTED_SHAPE); ldx >= K, ldd >= N (INVALID_ARG);
  *        x and ldx*2 bytes, codes and sf 16-byte aligned, bias and gscale 4-byte aligned, D
