@@ -2,8 +2,8 @@
 //
 //   y[m, n] = cast(G sum_k f(x[m, k]) e2m1(c[n, k]) e4m3(s[n, k / 16]) + bias[n])
 //
-// f is the identity or SiLU (rounded to x's type, as a separate kernel would leave it). HBM-bound:
-// the weight's 9/16 byte per value is read once for up to 16 rows of x.
+// f is the identity or SiLU. HBM-bound: the weight's 9/16 byte per value is read once for up to 16 rows
+// of x.
 //
 // The product runs on mma.sync.m16n8k16 (f16, float32 accumulators), weights as the 16-row operand
 // and up to 8 rows of x per instruction: with so few rows tcgen05 would need the weights decoded
@@ -12,7 +12,8 @@
 // between 2^-10 and 2688 and is exact in f16. x goes to f16 by a power of two for each 128 columns of a
 // row (their largest finite magnitude goes to [2^14, 2^15)): every bf16 value down to 2^-28 of that
 // stays exact and smaller ones are off by at most 2^-39 of it, below float32's own sums; infinities and
-// NaN stay what they are. So the arithmetic is that of float32 sums of exact products.
+// NaN stay what they are. So the arithmetic is that of float32 sums of exact products; SiLU's values are
+// rounded to f16 (2^-11 of each), once and less than a separate kernel that left them in bf16 would.
 //
 // A strip is 16 weight rows: rows r .. r+3 of each of the four 32-row quarters of a 128-row scale
 // tile. In the tensor-core scale layout the four quarters' scales of a row are adjacent, so a strip
@@ -85,7 +86,7 @@ __device__ __forceinline__ void gemv_unpack(const uint4& q, int f16, float (&f)[
 }
 
 // x / (1 + e^-x) in five instructions (about 2^-22 of the value, growing with |x| as the rounding of
-// x log2(e) does; it is rounded to 16 bits next).
+// x log2(e) does; it is rounded to f16 next).
 __device__ __forceinline__ float gemv_silu(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(-1.4426950408889634f * x)));
@@ -283,17 +284,14 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     each_vector([&](int v, uint4* p) {
       uint4 q = *p;
       float f[8];
-      if (a.silu) {  // rounded to x's type
-        gemv_unpack(q, a.x_f16, f);
+      gemv_unpack(q, a.x_f16, f);
+      if (a.silu) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = gemv_silu(f[k]);
-        q = a.x_f16 ? make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
-                                 pack_f16x2(f[6], f[7]))
-                    : make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                 pack_bf16x2(f[6], f[7]));
+        // for the largest magnitude only: a value that rounds up a power of two still fits f16
+        q = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
       }
-      gemv_unpack(q, a.x_f16, f);
-      float big = gemv_finite_amax(q, a.x_f16);
+      float big = gemv_finite_amax(q, a.x_f16 && !a.silu);
       const uint32_t half = 0xFFFFu << (lane & 16);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(half, big, o));

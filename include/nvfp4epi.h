@@ -298,8 +298,8 @@ nvfp4_status swiglu_bf16(const void* c, int64_t rows, int64_t nh, int64_t ldc,
  * the layout of those GEMMs' B operand; the activations stay in 16 bits.
  *   D[m, n] = cast(G sum_k f(x[m, k]) e2m1(codes[n, k]) e4m3(sf[n, k / 16]) + bias[n])
  *   x: M x K of x_dtype (NVFP4_OUT_BF16 or NVFP4_OUT_F16), leading dimension ldx.
- *   act: NVFP4_ACT_NONE (f the identity) or NVFP4_ACT_SILU (f(x) = x / (1 + exp(-x)), rounded to
- *        x's type as a separate kernel would leave it).
+ *   act: NVFP4_ACT_NONE (f the identity) or NVFP4_ACT_SILU (f(x) = x / (1 + exp(-x)), held in f16:
+ *        off by at most 2^-11 of itself).
  *   bias: N float32, or NULL.  D: M x N of out_dtype, leading dimension ldd elements.
  * Products are exact and sums float32; x is held in f16, scaled by a power of two for each 128 columns
  * of a row, which is exact for every value down to 2^-28 of their largest finite one and off by at most
