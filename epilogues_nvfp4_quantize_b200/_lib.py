@@ -381,7 +381,27 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
         _check(status, what)
 
 
+def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
+    """An uninitialised tensor that belongs to `stream` (None: the current one): its memory is neither
+    still in use by another stream's work nor handed to another one before this stream's work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 ACT_SILU = 2
+
+
+def _nvfp4(t: NVFP4Tensor) -> _Tensor:
+    """The C form of an NVFP4 tensor whose buffers are at least as large as its size says (an MXFP4
+    tensor's scales, one per 32 values, are not)."""
+    rows, cols = t.rows, t.cols
+    if 2 * t.codes.numel() < rows * cols or t.sf.numel() < (rows + 127) // 128 * 128 * ((cols + 63) // 64 * 4):
+        raise ValueError(f"codes or scales are too small for an NVFP4 tensor of {rows} x {cols}")
+    return t.c()
 
 
 def _pitch(stride, rows: int, cols: int) -> int:
@@ -407,7 +427,7 @@ def gemv_nvfp4(x: torch.Tensor, B: NVFP4Tensor, D: torch.Tensor, bias: Optional[
         raise ValueError("bias must be a contiguous float32 tensor with one value per row of B")
     dev = _same_device(x, D, B.codes, B.sf, B.gscale, bias)
     _call((_lib or load()).gemv_nvfp4, "gemv_nvfp4", dev, stream, x.data_ptr(), _OUT_KIND[x_dtype], M,
-          _pitch(sx, M, K), ACT_SILU if silu else ACT_NONE, B.c(), None if bias is None else bias.data_ptr(),
+          _pitch(sx, M, K), ACT_SILU if silu else ACT_NONE, _nvfp4(B), None if bias is None else bias.data_ptr(),
           _OUT_KIND[D_dtype], D.data_ptr(), _pitch(sD, M, N))
     return D
 
@@ -494,7 +514,7 @@ def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, hq: Optiona
     shape = x.shape
     _stats(stats, shape[0])
     _call((_lib or load()).residual_norm, "residual_norm", dev, stream, a, *_matrix(x_out, "x_out", shape, x.dtype),
-          *_matrix(h, "h", shape, torch.bfloat16), ctypes.pointer(hq.c()) if hq is not None else None,
+          *_matrix(h, "h", shape, torch.bfloat16), ctypes.pointer(_nvfp4(hq)) if hq is not None else None,
           None if stats is None else stats.data_ptr())
     return x_out, h, hq
 
@@ -536,7 +556,7 @@ def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: 
     if seq is not None or dw is not None or dw_post is not None:
         need = residual_norm_workspace_bytes(rows, cols, shape[0])
         if workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=x_out.device)
+            workspace = _empty_on(stream, (need,), torch.uint8, x_out.device)
         elif workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
     _call((_lib or load()).residual_norm_backward, "residual_norm_backward", dev, stream, a, stats.data_ptr(), g,
@@ -628,14 +648,14 @@ def _axis_pairs(pairs: tuple):
 def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pairs, y: Optional[torch.Tensor] = None,
               interleaved: bool = True, inverse: bool = False, stream=None) -> torch.Tensor:
     """Rotary positions on heads x (rows x heads x head_dim; bf16, f16 or f32) into y, which may be
-    x itself (None: a new contiguous tensor). positions: rows x axes, int32 or float32; pairs: how
+    x itself (None: a new contiguous tensor, allocated on `stream`). positions: rows x axes, int32 or float32; pairs: how
     many pairs each axis turns; freqs: one float64 per pair (rope_frequencies). inverse: the
     opposite rotation, which is also the gradient (see rope_axes in the header)."""
     dtype, sx, shape = x.dtype, x.stride(), x.shape
     if len(sx) != 3 or sx[2] != 1 or dtype not in _OUT_KIND:
         raise ValueError("x must be a rows x heads x head_dim tensor (bf16, f16 or f32) with unit last stride")
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
+        y = _empty_on(stream, shape, dtype, x.device)
     sy = y.stride()
     if y.shape != shape or y.dtype is not dtype or sy[2] != 1:
         raise ValueError("y must have x's shape and type and unit last stride")

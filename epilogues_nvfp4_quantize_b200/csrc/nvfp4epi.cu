@@ -966,7 +966,7 @@ NVFP4_API nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t
   if (!is_dtype(out_dtype)) return NVFP4_ERR_INVALID_ARG;
   nvfp4_status st;
   if ((st = check_operand(B)) != NVFP4_OK) return st;
-  if (M <= 0 || M > (1ll << 19) || B.rows > (1ll << 31) || B.cols % 64 != 0 || B.cols > 32768)
+  if (M <= 0 || M > 524280 || B.rows > (1ll << 31) || B.cols % 64 != 0 || B.cols > 32768)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (ldx < B.cols || ldd < B.rows) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(x) || ldx % 8 != 0 || !aligned_to(D, static_cast<uintptr_t>(out_size(out_dtype))) ||
@@ -1159,7 +1159,7 @@ NVFP4_API nvfp4_status residual_norm(const nvfp4_norm_inputs* in, void* x_out, i
   if (x_out == nullptr && h == nullptr && hq == nullptr && stats == nullptr) return NVFP4_ERR_INVALID_ARG;
   if (in->norm == NVFP4_NORM_NONE && (h != nullptr || hq != nullptr)) return NVFP4_ERR_INVALID_ARG;
   if ((x_out != nullptr && ldxo < in->cols) || (h != nullptr && ldh < in->cols)) return NVFP4_ERR_INVALID_ARG;
-  if (x_out == in->x && ldxo != in->ldx) return NVFP4_ERR_INVALID_ARG;
+  if (x_out == in->x && ldxo != in->ldx && in->rows > 1) return NVFP4_ERR_INVALID_ARG;
   if (!aligned16(x_out) || (x_out != nullptr && (ldxo * out_size(in->stream_dtype)) % 16 != 0) || !aligned16(h) ||
       (h != nullptr && ldh % 8 != 0) || !aligned16(stats))
     return NVFP4_ERR_MISALIGNED;
@@ -1245,6 +1245,11 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
       !aligned_to(g->dgate, 4) || !aligned_to(g->dscale, 4) || !aligned_to(g->dshift, 4) || !aligned_to(g->dw, 4) ||
       !aligned_to(g->dw_post, 4) || !aligned16(workspace))
     return NVFP4_ERR_MISALIGNED;
+  // in place only where a row's output lies on its own input
+  if (in->rows > 1 && ((g->dx != nullptr && g->dx == g->dx_out && g->lddx != g->lddxo) ||
+                       (g->dy != nullptr && ((g->dy == g->dh && g->lddy != g->lddh) ||
+                                             (g->dy == in->y && g->lddy != in->ldy)))))
+    return NVFP4_ERR_INVALID_ARG;
   int dev;
   DeviceInfo* info;
   if ((st = current_device(&dev, &info)) != NVFP4_OK) return st;

@@ -304,10 +304,10 @@ nvfp4_status swiglu_bf16(const void* c, int64_t rows, int64_t nh, int64_t ldc,
  * Products are exact and sums float32; x is held in f16, scaled by a power of two for each 128 columns
  * of a row, which is exact for every value down to 2^-28 of their largest finite one and off by at most
  * 2^-39 of that below. Infinities and NaN in x reach the outputs of their row only.
- * Rules: M >= 1 (rows are taken 16 at a time: past 16, the weight is read again for each 16 rows),
- *        N >= 1, K % 64 == 0, K <= 32768 (UNSUPPORTED_SHAPE); ldx >= K, ldd >= N (INVALID_ARG);
+ * Rules: 1 <= M <= 524280 (rows are taken 16 at a time: past 16, the weight is read again for each
+ *        16 rows), N >= 1, K % 64 == 0, K <= 32768 (UNSUPPORTED_SHAPE); ldx >= K, ldd >= N (INVALID_ARG);
  *        x and ldx*2 bytes, codes and sf 16-byte aligned, bias and gscale 4-byte aligned, D
- *        aligned to its element (MISALIGNED).
+ *        aligned to its element (MISALIGNED). D may not overlap an input.
  */
 #define NVFP4_ACT_SILU 2
 nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t ldx, int act, nvfp4_tensor B,
@@ -381,7 +381,7 @@ nvfp4_status residual_norm(const nvfp4_norm_inputs* in, void* x_out, int64_t ldx
  *   workspace: residual_norm_workspace_bytes(rows, cols, batches) bytes, 16-byte aligned, contents
  *              ignored on entry; calls that share one must not overlap on the GPU. It may be NULL
  *              when none of dgate, dscale, dshift, dw and dw_post is asked for.
- * Rules as residual_norm; dx may be dx_out (same pitch), dy may be dh or y.
+ * Rules as residual_norm; dx may be dx_out, and dy may be dh or y, with the same pitch.
  */
 typedef struct {
   const void* dx_out;

@@ -171,6 +171,46 @@ def test_training_operators_together():
         assert (np.abs(f64(t.grad) - ref[k]) <= tol).all(), k
 
 
+def test_a_training_step_captured_and_replayed():
+    """Forward and backward of the operators together in one graph: replays give the eager step's bits,
+    for the inputs that are in the buffers then."""
+    rows, heads, hd, pairs = 96, 4, 64, [12, 20]
+    cols = heads * hd
+    g = torch.Generator().manual_seed(5)
+    rn = lambda *s: torch.randn(*s, generator=g).to(device())  # noqa: E731
+    x, y, c = rn(rows, cols), rn(rows, cols).bfloat16(), rn(rows, heads, hd).bfloat16()
+    gate, scale, shift = (0.5 * rn(3, cols) for _ in range(3))
+    w, w_post = 1 + 0.1 * rn(cols), 1 + 0.1 * rn(cols)
+    offsets = torch.tensor([0, 30, 30, 90], dtype=torch.int32, device=device())
+    pos = torch.randint(0, 64, (rows, 2), generator=g).int().to(device())
+    freqs = ep.rope_frequencies(pairs, device=device())
+
+    def step():
+        leaves = [t.detach().requires_grad_(True) for t in (x, y, gate, scale, shift, w, w_post)]
+        x_out, h = ep.ResidualNorm.apply(*leaves, "layer", True, 1.0, 1e-6, offsets)
+        r = ep.RopeAxes.apply(h.view(rows, heads, hd), pos, freqs, pairs)
+        return [x_out.detach(), r.detach()] + list(torch.autograd.grad([x_out, r], leaves, [x.detach(), c]))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (6, 7):
+        g.manual_seed(seed)
+        x.copy_(rn(rows, cols)), y.copy_(rn(rows, cols)), scale.copy_(rn(3, cols))
+        want = step()
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert ep.read_device_status() == 0
+
+
 def test_offsets_past_32_bits():
     """Rows 2^31 elements apart: every operator's addresses in 64 bits."""
     pitch = 2 ** 31

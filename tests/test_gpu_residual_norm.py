@@ -153,6 +153,8 @@ MANY_ROWS = [
     (502, 16384, 2, dict(stream="f32", w=True)),
     (940, 4032, 2, dict(norm=None, post=True, w=True, alpha=0.5)),
     (940, 3968, 5, dict(norm=None)),
+    (1600, 256, 1600, dict(post=True, w=True)),  # a modulation vector for each row
+    (1600, 9000, 1600, dict(mod="f32")),
 ]
 
 
@@ -227,12 +229,23 @@ def check_gradient(x_out, a, b, B, dxo, dh, got):
                                     p["w_post"], a["residual_scale"], a["norm"], p["w"], p["scale"])
     live = b >= 0
     rows = x_out.shape[0]
+    # dscale and dw: xhat = (x' - mean) rstd is off by rstd (64 u mean|x'| + 2 u |x'|) besides its 40 u |xhat|
+    # (as h above), and a sum over rows by |dh w| or |dh (1 + scale)| times that; where a sequence has one
+    # row and x' is next to its mean, that is more than any multiple of u |dh xhat|
+    extra = {}
+    if dh is not None:
+        z = f64(x_out)[live]
+        d = np.abs(f64(dh)[live]) * lo.stats(f64(x_out), a["norm"])[1][live] * (
+            64 * U * np.abs(z).mean(1, keepdims=True) + 2 * U * np.abs(z))
+        extra["dscale"] = np.zeros((B, z.shape[1]))
+        np.add.at(extra["dscale"], b[live], d * (1.0 if p["w"] is None else np.abs(p["w"])))
+        extra["dw"] = (d * (1.0 if p["scale"] is None else np.abs(1 + p["scale"][b[live]]))).sum(0)
     for k, t in got.items():
         if k in ("dx", "dy"):
             within(t[live], ref[k][live], (256 if k == "dx" else 512) * U * ref["size_" + k][live], half(t), k)
             assert bool((t[~live] == 3.0).all()), f"{k}: rows without a sequence"
         elif k in ref:
-            within(t, ref[k], (512 + rows / 64 + 300) * U * ref["size_" + k], U, k)
+            within(t, ref[k], (512 + rows / 64 + 300) * U * ref["size_" + k] + extra.get(k, 0.0), U, k)
         else:  # no dh: the norm contributes nothing
             assert bool((t == 0).all()), k
 
@@ -243,6 +256,10 @@ GRAD_CASES = [c for c in CASES if c[1] <= 8200] + [
     (3000, 72, 3, dict(offsets=[0, 1, 2900, 2950], post=True, w=True, stream="f32")),
     (64, 64, 64, dict(post=True, w=True)),  # a modulation vector for each row
     (3, 16384, 1, dict(post=True, w=True, norm="rms")),
+    (2400, 256, 2400, dict(w=True, stream="f32")),
+    (400, 5120, 4, dict(offsets=[1, 1, 200, 260, 390], post=True, w=True)),  # clusters that walk several rows
+    (290, 8200, 2, dict(stream="f32", mod="f32", w=True)),
+    (129, 16384, 3, dict(stream="f32", post=True, w=True, norm="rms")),
 ]
 
 
@@ -268,6 +285,31 @@ def test_gradient(rows, cols, B, opt):
         if a["y"] is not None:
             part = grads(x_out, stats, a, b, B, dxo, None, only=("dy", "dgate", "dscale"))
             check_gradient(x_out, a, b, B, dxo, None, part)
+
+
+@pytest.mark.parametrize("rows,cols", [(60, 256), (1500, 512), (200, 5120)])
+def test_what_stands_in_rows_without_a_sequence_reaches_nothing(rows, cols):
+    """NaN and infinities in the rows in front of the first and behind the last sequence: outputs and
+    gradients are those of the same call with zeros there, the parameters' among them."""
+    off = [3, rows // 2, rows // 2, rows - 7]
+    x, a, b = make(rows, cols, 3, offsets=off, post=True, w=True)
+    live = torch.from_numpy(b >= 0).to(device())[:, None]
+
+    def run(fill):
+        put = lambda t: torch.where(live, t, torch.full_like(t, fill))  # noqa: E731
+        c = dict(a, y=put(a["y"]))
+        g = torch.Generator().manual_seed(3)
+        dxo, dh = (put(torch.randn(rows, cols, generator=g).bfloat16().to(device())) for _ in range(2))
+        h = torch.full((rows, cols), 5.0, dtype=torch.bfloat16, device=device())
+        xo, stats = put(torch.zeros_like(h)), put(torch.zeros(rows, 1, device=device())).expand(rows, 4).contiguous()
+        ep.residual_norm(put(x), h, x_out=xo, stats=stats, **c)
+        out = grads(xo, stats, c, b, 3, dxo, dh)
+        return [t for k, t in out.items()] + [h, torch.where(live, xo, torch.zeros_like(xo))]
+
+    want = run(0.0)
+    for fill in (float("nan"), float("inf")):
+        assert all(torch.equal(p, q) for p, q in zip(run(fill), want))
+    assert all(bool(torch.isfinite(t).all()) for t in want)
 
 
 def test_gradient_in_place():
@@ -325,6 +367,34 @@ def test_autograd_function_parts(which):
         within(shift.grad, ref["dshift"], 820 * U * ref["size_dshift"], U, "dshift")
     elif norm is not None:
         assert bool((shift.grad == 0).all())
+
+
+def test_a_workspace_belongs_to_the_stream_of_its_call(monkeypatch):
+    x, a, b = make(100, 512, 2, post=True, w=True)
+    xo, stats = torch.empty(100, 512, dtype=x.dtype, device=device()), torch.empty(100, 4, device=device())
+    ep.residual_norm(x, torch.empty_like(xo), x_out=xo, stats=stats, batches=2, **a)
+    dh = torch.randn_like(xo)
+    want = torch.empty(2, 512, device=device())
+    args = {k: v for k, v in a.items() if k != "shift"}
+    ep.residual_norm_backward(xo, stats, dh=dh, batches=2, dgate=want, **args)
+    torch.cuda.synchronize()
+    made_on, empty = [], torch.empty
+
+    def spy(*p, **k):
+        made_on.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*p, **k)
+
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):  # an object, and a plain handle
+        got = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        monkeypatch.setattr(torch, "empty", spy)
+        ep.residual_norm_backward(xo, stats, dh=dh, batches=2, dgate=got, stream=stream, **args)
+        monkeypatch.undo()
+        s.synchronize()
+        assert torch.equal(got, want)
+    assert made_on == [s.cuda_stream] * 2
+    assert torch.cuda.current_stream().cuda_stream != s.cuda_stream
 
 
 def test_gradient_from_a_graph():

@@ -129,6 +129,12 @@ def test_other_stream_and_graph():
     ep.rope_axes(x, pos, freqs, pairs, y, stream=s)
     s.synchronize()
     assert torch.equal(y, want)
+    made = ep.rope_axes(x, pos, freqs, pairs, stream=s)
+    s.synchronize()
+    assert torch.equal(made, want)
+    at = made.data_ptr()
+    owners = [g["stream"] for g in torch.cuda.memory_snapshot() if g["address"] <= at < g["address"] + g["total_size"]]
+    assert owners == [s.cuda_stream]  # its memory is the stream's own
     z = torch.zeros_like(x)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

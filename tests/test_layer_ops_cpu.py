@@ -117,7 +117,7 @@ def test_gemv_argument_checks(lib):
     assert call(xt=2) == INVALID and call(xt=-1) == INVALID and call(ot=3) == INVALID
     assert call(act=1) == INVALID  # ReLU belongs to the pointwise epilogue
     assert call(B=_t(codes=0)) == INVALID
-    assert call(M=0) == SHAPE and call(B=_t(rows=0)) == SHAPE and call(B=_t(cols=0)) == SHAPE
+    assert call(M=0) == SHAPE and call(M=524281) == SHAPE and call(B=_t(rows=0)) == SHAPE and call(B=_t(cols=0)) == SHAPE
     assert call(B=_t(cols=96), ldx=96) == SHAPE and call(B=_t(cols=32768 + 64), ldx=40000) == SHAPE
     assert call(ldx=120) == INVALID and call(ldd=255) == INVALID
     assert call(x=24) == MISALIGNED and call(ldx=132) == MISALIGNED
@@ -178,6 +178,10 @@ def test_residual_norm_backward_argument_checks(lib):
     assert call(dy=16, lddy=64) == INVALID and call(dgate=16, lddgate=64) == INVALID  # no branch
     assert call(dw_post=16, i=dict(y=16, ldy=64)) == INVALID
     assert call(dscale=16, lddscale=64, ws=None) == INVALID
+    # in place with another pitch
+    assert call(dx=16, lddx=128) == INVALID
+    assert call(dx=None, dy=16, lddy=128, i=dict(y=32, ldy=64)) == INVALID
+    assert call(dx=None, dy=32, lddy=128, i=dict(y=32, ldy=64)) == INVALID
     assert call(lddx=56) == INVALID and call(dshift=16, lddshift=56) == INVALID
     assert call(dx=24) == MISALIGNED and call(dh=24) == MISALIGNED and call(lddxo=68) == MISALIGNED
     assert call(ws=8, dscale=16, lddscale=64) == MISALIGNED and call(dw=18) == MISALIGNED
@@ -219,6 +223,11 @@ def test_python_calls_refuse_wrong_tensors(lib):
             ep.gemv_nvfp4(x, B, bad)
     with pytest.raises(ValueError):
         ep.gemv_nvfp4(x, B, D, bias=torch.zeros(8, dtype=bf))
+
+    for codes, sf in ((B.codes[:7], B.sf), (B.codes, B.sf[:256])):  # the second is an MXFP4 tensor's
+        with pytest.raises(ValueError, match="too small"):
+            _lib._nvfp4(_lib.NVFP4Tensor(codes, sf, B.gscale, 8, 64))
+    assert _lib._nvfp4(B).rows == 8
 
     h = torch.zeros(2, 64, dtype=bf)
     with pytest.raises(ValueError, match="CUDA"):
