@@ -427,8 +427,9 @@ def gemv_nvfp4(x: torch.Tensor, B: NVFP4Tensor, D: torch.Tensor, bias: Optional[
         raise ValueError("bias must be a contiguous float32 tensor with one value per row of B")
     dev = _same_device(x, D, B.codes, B.sf, B.gscale, bias)
     _call((_lib or load()).gemv_nvfp4, "gemv_nvfp4", dev, stream, x.data_ptr(), _OUT_KIND[x_dtype], M,
-          _pitch(sx, M, K), ACT_SILU if silu else ACT_NONE, _nvfp4(B), None if bias is None else bias.data_ptr(),
-          _OUT_KIND[D_dtype], D.data_ptr(), _pitch(sD, M, N))
+          sx[0] if M > 1 else _pitch(sx, M, K), ACT_SILU if silu else ACT_NONE, _nvfp4(B),
+          None if bias is None else bias.data_ptr(), _OUT_KIND[D_dtype], D.data_ptr(),
+          sD[0] if M > 1 else _pitch(sD, M, N))
     return D
 
 
@@ -439,19 +440,20 @@ _NORM_INPUTS = struct.Struct("@3qP4i2f" + "Pq" * 5 + "2P")
 _NORM_GRADS = struct.Struct("@" + "Pq" * 7 + "2P")
 
 
-def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
-    """Pointer and row pitch of an optional 2-D tensor of the given shape and type."""
-    if t is None:
-        return 0, 0
-    s = t.stride()
-    if t.dtype is not dtype or t.shape != shape or s[1] != 1:
+def _matrix(t: torch.Tensor, name: str, shape, dtype):
+    """Pointer and row pitch of a 2-D tensor of the given shape and type."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {shape[0]} x {shape[1]} {dtype} tensor with unit column stride")
-    return t.data_ptr(), _pitch(s, *shape)
+    pitch, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must be a {shape[0]} x {shape[1]} {dtype} tensor with unit column stride")
+    return t.data_ptr(), pitch if shape[0] > 1 else _pitch((pitch,), 1, shape[1])
 
 
-def _vector(t: Optional[torch.Tensor], name: str, cols: int):
-    if t is None:
-        return 0
+_NONE = (0, 0)  # the pointer and pitch of a matrix that is not given
+
+
+def _vector(t: torch.Tensor, name: str, cols: int):
     if t.dtype is not torch.float32 or t.shape != (cols,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {cols} values")
     return t.data_ptr()
@@ -481,14 +483,16 @@ def _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_
     shape = (batches, cols)
     return _NORM_INPUTS.pack(
         rows, cols, batches, 0 if offsets is None else offsets.data_ptr(), _OUT_KIND[x_dtype], _OUT_KIND[mod_dtype],
-        _NORMS[norm], post_norm, residual_scale, eps, x.data_ptr(), _pitch(sx, rows, cols),
-        *_matrix(y, "y", x_shape, torch.bfloat16), *_matrix(gate, "gate", shape, mod_dtype),
-        *_matrix(scale, "scale", shape, mod_dtype), *_matrix(shift, "shift", shape, mod_dtype),
-        _vector(w_post, "w_post", cols), _vector(w, "w", cols)), shape
+        _NORMS[norm], post_norm, residual_scale, eps, x.data_ptr(), sx[0] if rows > 1 else _pitch(sx, rows, cols),
+        *(_NONE if y is None else _matrix(y, "y", x_shape, torch.bfloat16)),
+        *(_NONE if gate is None else _matrix(gate, "gate", shape, mod_dtype)),
+        *(_NONE if scale is None else _matrix(scale, "scale", shape, mod_dtype)),
+        *(_NONE if shift is None else _matrix(shift, "shift", shape, mod_dtype)),
+        0 if w_post is None else _vector(w_post, "w_post", cols), 0 if w is None else _vector(w, "w", cols)), shape
 
 
 def _stats(stats, rows):
-    if stats is not None and (stats.dtype is not torch.float32 or stats.shape != (rows, 4) or not stats.is_contiguous()):
+    if stats.dtype is not torch.float32 or stats.shape != (rows, 4) or not stats.is_contiguous():
         raise ValueError("stats must be a contiguous rows x 4 float32 tensor")
 
 
@@ -508,13 +512,16 @@ def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, hq: Optiona
     int32 row offsets on the device (None: sequences of equal length); rows without a sequence are
     left as they are. stats: rows x 4 float32, written for residual_norm_backward. Outputs that are
     None are not written. Returns (x_out, h, hq)."""
-    dev = _same_device(x, h, y, x_out, gate, w_post, w, scale, shift, offsets, stats,
-                       *((hq.codes, hq.sf, hq.gscale) if hq is not None else ()))
+    dev = _same_device(x, h, y, x_out, gate, w_post, w, scale, shift, offsets, stats)
+    if hq is not None:
+        _same_device(x, hq.codes, hq.sf, hq.gscale)
     a, _ = _norm_inputs(x, y, gate, scale, shift, w, w_post, norm, post_norm, residual_scale, eps, offsets, batches)
     shape = x.shape
-    _stats(stats, shape[0])
-    _call((_lib or load()).residual_norm, "residual_norm", dev, stream, a, *_matrix(x_out, "x_out", shape, x.dtype),
-          *_matrix(h, "h", shape, torch.bfloat16), ctypes.pointer(_nvfp4(hq)) if hq is not None else None,
+    if stats is not None:
+        _stats(stats, shape[0])
+    _call((_lib or load()).residual_norm, "residual_norm", dev, stream, a,
+          *(_NONE if x_out is None else _matrix(x_out, "x_out", shape, x.dtype)),
+          *(_NONE if h is None else _matrix(h, "h", shape, torch.bfloat16)), ctypes.pointer(_nvfp4(hq)) if hq is not None else None,
           None if stats is None else stats.data_ptr())
     return x_out, h, hq
 
@@ -548,11 +555,15 @@ def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: 
     full, dtype, bf16, f32 = x_out.shape, x_out.dtype, torch.bfloat16, torch.float32
     rows, cols = full
     _stats(stats, rows)
-    g = _NORM_GRADS.pack(*_matrix(dx_out, "dx_out", full, dtype), *_matrix(dh, "dh", full, bf16),
-                         *_matrix(dx, "dx", full, dtype), *_matrix(dy, "dy", full, bf16),
-                         *_matrix(dgate, "dgate", shape, f32), *_matrix(dscale, "dscale", shape, f32),
-                         *_matrix(dshift, "dshift", shape, f32), _vector(dw, "dw", cols),
-                         _vector(dw_post, "dw_post", cols))
+    g = _NORM_GRADS.pack(*(_NONE if dx_out is None else _matrix(dx_out, "dx_out", full, dtype)),
+                         *(_NONE if dh is None else _matrix(dh, "dh", full, bf16)),
+                         *(_NONE if dx is None else _matrix(dx, "dx", full, dtype)),
+                         *(_NONE if dy is None else _matrix(dy, "dy", full, bf16)),
+                         *(_NONE if dgate is None else _matrix(dgate, "dgate", shape, f32)),
+                         *(_NONE if dscale is None else _matrix(dscale, "dscale", shape, f32)),
+                         *(_NONE if dshift is None else _matrix(dshift, "dshift", shape, f32)),
+                         0 if dw is None else _vector(dw, "dw", cols),
+                         0 if dw_post is None else _vector(dw_post, "dw_post", cols))
     if seq is not None or dw is not None or dw_post is not None:
         need = residual_norm_workspace_bytes(rows, cols, shape[0])
         if workspace is None:
@@ -655,7 +666,8 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pai
     if len(sx) != 3 or sx[2] != 1 or dtype not in _OUT_KIND:
         raise ValueError("x must be a rows x heads x head_dim tensor (bf16, f16 or f32) with unit last stride")
     if y is None:
-        y = _empty_on(stream, shape, dtype, x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if stream is None else (
+            _empty_on(stream, shape, dtype, x.device))
     sy = y.stride()
     if y.shape != shape or y.dtype is not dtype or sy[2] != 1:
         raise ValueError("y must have x's shape and type and unit last stride")
