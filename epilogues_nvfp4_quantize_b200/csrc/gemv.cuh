@@ -37,6 +37,8 @@ constexpr int TILE_TOKENS = 16;       // rows of x per pass over the weight
 constexpr int ROUND = 16;             // strips between two joins of a cluster
 constexpr int SLOT = 32 * (2 * 16 + 2 * 4);  // bytes of a step in shared memory: 16 + 16 of codes, 4 + 4 of scales a lane
 constexpr int MAX_CLUSTER = 8;
+constexpr int PAIR_TOKENS = 2;        // rows of x up to which block scales multiply sums instead of weights
+constexpr int ZEROS = 256;            // bytes of 0 in shared memory, for that
 constexpr int MAX_SMEM = 220 * 1024;
 }  // namespace gemvcfg
 
@@ -67,7 +69,8 @@ __host__ __device__ constexpr int gemv_smem(int nt, int depth, int64_t tokens, i
   return gemvcfg::WARPS * depth * gemvcfg::SLOT +                                                // ring of weights
          2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? gemvcfg::ROUND * 512 * nt : 0) +         // joins
          kslice / gemvcfg::GROUP * 8 * nt * 4 +                                                  // factors of x
-         static_cast<int>(tokens < 8 * nt ? tokens : 8 * nt) * gemv_x_pitch(kslice);             // x
+         static_cast<int>(tokens < 8 * nt ? tokens : 8 * nt) * gemv_x_pitch(kslice) +            // x
+         (tokens <= gemvcfg::PAIR_TOKENS ? gemvcfg::ZEROS : 0);
 }
 
 __device__ __forceinline__ void gemv_unpack(const uint4& q, int f16, float (&f)[8]) {
@@ -173,7 +176,8 @@ __device__ __forceinline__ void copy_async_wait() {
 }
 
 // DEPTH (a power of two): steps of codes and scales in flight per warp.
-template <int NT, int DEPTH>
+// PAIR: at most two rows of x.
+template <int NT, int DEPTH, bool PAIR>
 __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const GemvArgs a) {
   using namespace gemvcfg;
   extern __shared__ __align__(128) uint8_t gemv_smem_raw[];
@@ -307,6 +311,9 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
   }
 #pragma unroll
   for (int j = FIRST; j < DEPTH; ++j) load(my_ring + j * SLOT);
+  if constexpr (PAIR) {
+    if (tid < ZEROS / 16) reinterpret_cast<uint4*>(xs + tokens * pitch)[tid] = make_uint4(0u, 0u, 0u, 0u);
+  }
   __syncthreads();
 
   // ---- products -------------------------------------------------------------------------
@@ -320,6 +327,54 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
   const uint8_t* xlane[NT];  // rows past the tokens read the last one: their columns are not stored
 #pragma unroll
   for (int n = 0; n < NT; ++n) xlane[n] = xs + (8 * n + g < tokens ? 8 * n + g : tokens - 1) * pitch + gb * 256 + t * 16;
+  // One or two rows of x: the operand's eight columns are rows of x times lanes t, column 2 t + m holding
+  // row m at lane t's places of K and 0 elsewhere. A sum then covers one lane's columns only, that is one
+  // scale block per row in four instructions, and is multiplied by that block's scale: 12 float32
+  // instructions per step instead of 32 f16 products, and weights go to the tensor core as they are decoded.
+  // (2 x 4096 x 24576: 20.1 -> 19.2 us.)
+  const uint8_t* const zeros = xs + tokens * pitch;
+  const bool holds = (g >> 1) == t;
+  const uint8_t* const xpair = holds ? xs + ((g & 1) < tokens ? g & 1 : 0) * pitch + gb * 256 + t * 16 : zeros + t * 16;
+  const int xpair_step = holds ? 256 : 0;
+  auto compute_pair = [&](int step, const uint8_t* slot) {
+    float2 sc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h2;
+      const uint16_t two = *reinterpret_cast<const uint16_t*>(slot + 1024 + 128 * i + lane * 4 + (t & 1) * 2);
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+      sc[i] = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    }
+    const uint4 q0 = *reinterpret_cast<const uint4*>(slot + lane * 16);
+    const uint4 q1 = *reinterpret_cast<const uint4*>(slot + 512 + lane * 16);
+    const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w};
+    const uint32_t c1[4] = {q1.x, q1.y, q1.z, q1.w};
+    const uint8_t* const xp = xpair + step * xpair_step;
+    float sum[2][4];  // of the lane's two blocks
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {  // the two blocks in turn: neither waits for the other's sum
+        const int w = 2 * b + h;
+        uint32_t a0[4], a1[4];
+        e2m1x8_to_f16x2(c0[w], a0);
+        e2m1x8_to_f16x2(c1[w], a1);
+        const uint4 xb = *reinterpret_cast<const uint4*>(xp + w * 64);
+        if (h == 0) {
+          mma_16x8x16_from0(sum[b], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+        } else {
+          mma_16x8x16(sum[b], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+        }
+        mma_16x8x16(sum[b], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+      }
+    }
+    const float2 f = *reinterpret_cast<const float2*>(inv + (gb + step) * 8 * NT);  // of rows 0 and 1
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 s = sc[i >> 1];
+      acc[0][i] = fmaf(fmaf(sum[1][i], s.y, sum[0][i] * s.x), i & 1 ? f.y : f.x, acc[0][i]);
+    }
+  };
   auto compute = [&](int step, const uint8_t* slot) {
     uint32_t s2[2][2];
 #pragma unroll
@@ -364,7 +419,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
       for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(one[n][i], i & 1 ? f.y : f.x, acc[n][i]);
     }
   };
-  // Value i of lane's fragment: weight row g or g + 8 of the strip, row 2 t or 2 t + 1 of x
+  // Value i of lane's fragment: weight row g or g + 8 of the strip, row 2 t or 2 t + 1 of x (PAIR: row 0 or 1)
   float bias[2] = {0.0f, 0.0f};
   auto load_bias = [&](int strip) {
     const int64_t row = static_cast<int64_t>(strip >> 3) * 128 + (g >> 2) * 32 + (strip & 7) * 4 + (g & 3);
@@ -374,7 +429,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     }
   };
   auto put = [&](int strip, int n, int i, float v) {
-    const int m = 8 * n + 2 * t + (i & 1);
+    const int m = PAIR ? 2 * 8 * t + (i & 1) : 8 * n + 2 * t + (i & 1);  // PAIR: lanes t > 0 hold the same
     const int64_t row = static_cast<int64_t>(strip >> 3) * 128 + (g >> 2) * 32 + (i >> 1) * 64 + (strip & 7) * 4 + (g & 3);
     if (m >= tokens || row >= a.N) return;
     v += bias[i >> 1];
@@ -428,7 +483,13 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     }
     if (mine) {
 #pragma unroll
-      for (int i = 0; i < 4 * NT; ++i) sum[i] *= G;
+      for (int i = 0; i < 4 * NT; ++i) {
+        if constexpr (PAIR) {  // the lanes' blocks
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        }
+        sum[i] *= G;
+      }
       if (cluster == 1) {
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i) put(strip, i >> 2, i & 3, sum[i]);
@@ -480,7 +541,13 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     if (cluster == 1 && wk == (it & (kwarps - 1)) && strip < a.strips) load_bias(strip);
     for (int step = 0; step < a.per; ++step) {
       copy_async_wait<DEPTH - 1>();
-      if (gb + step < groups) compute(step, ring_warp + slot * SLOT);
+      if (gb + step < groups) {
+        if constexpr (PAIR) {
+          compute_pair(step, ring_warp + slot * SLOT);
+        } else {
+          compute(step, ring_warp + slot * SLOT);
+        }
+      }
       load(my_ring + slot * SLOT);
       slot = (slot + 1) & (DEPTH - 1);
     }

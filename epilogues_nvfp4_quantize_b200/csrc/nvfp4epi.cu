@@ -45,7 +45,7 @@ struct DeviceInfo {
   // clusters of gemv_nvfp4_kernel that fit at once, by log2 of the cluster size (all instances take
   // one CTA per SM)
   int gemv_clusters[4] = {};
-  bool gemv_attr_set[2] = {};
+  bool gemv_attr_set[3] = {};
   int norm_regs[8] = {};             // registers of residual_norm_ring_kernel, by stream type, NV and POST
   bool norm_grad_attr_set[8] = {};   // residual_norm_grad_kernel, by stream type, POST and CLUSTER
 };
@@ -874,10 +874,10 @@ nvfp4_status launch_dependent(void (*kern)(Args), dim3 grid, int threads, size_t
 
 bool is_dtype(int d) { return d == NVFP4_OUT_BF16 || d == NVFP4_OUT_F16 || d == NVFP4_OUT_F32; }
 
-template <int NT>
+template <int NT, bool PAIR>
 nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t stream) {
   using namespace nvfp4::gemvcfg;
-  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 8>, nvfp4::gemv_nvfp4_kernel<NT, 4>};
+  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 8, PAIR>, nvfp4::gemv_nvfp4_kernel<NT, 4, PAIR>};
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
@@ -891,7 +891,8 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   int clusters[4];
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (!info->gemv_attr_set[NT - 1]) {
+    bool& set = info->gemv_attr_set[PAIR ? 0 : NT];
+    if (!set) {
       for (auto kern : kerns) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM) != cudaSuccess)
           return NVFP4_ERR_CUDA;
@@ -905,7 +906,7 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
         if (cudaOccupancyMaxActiveClusters(&n, kerns[0], &cfg) != cudaSuccess || n <= 0) return NVFP4_ERR_CUDA;
         info->gemv_clusters[i] = n;
       }
-      info->gemv_attr_set[NT - 1] = true;
+      set = true;
     }
     std::memcpy(clusters, info->gemv_clusters, sizeof(clusters));
   }
@@ -992,8 +993,9 @@ NVFP4_API nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t
   a.out_kind = out_dtype;
   a.strips = static_cast<int>((B.rows + 127) / 128 * 8);
   // 16 rows at a time, or 8 where 16 rows of a very long K do not fit in a cluster's shared memory
-  st = M > 8 ? launch_gemv<2>(info, a, stream) : NVFP4_ERR_UNSUPPORTED_SHAPE;
-  return st == NVFP4_ERR_UNSUPPORTED_SHAPE ? launch_gemv<1>(info, a, stream) : st;
+  if (M <= nvfp4::gemvcfg::PAIR_TOKENS) return launch_gemv<1, true>(info, a, stream);
+  st = M > 8 ? launch_gemv<2, false>(info, a, stream) : NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return st == NVFP4_ERR_UNSUPPORTED_SHAPE ? launch_gemv<1, false>(info, a, stream) : st;
 }
 
 namespace {
