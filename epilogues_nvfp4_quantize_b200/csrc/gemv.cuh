@@ -35,7 +35,8 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int GROUP = 128;            // columns of K per step of a warp
 constexpr int TILE_TOKENS = 16;       // rows of x per pass over the weight
 constexpr int ROUND = 16;             // strips between two joins of a cluster
-constexpr int SLOT = 32 * (2 * 16 + 2 * 4);  // bytes of a step in shared memory: 16 + 16 of codes, 4 + 4 of scales a lane
+constexpr int STEPS = 2;              // steps whose weights are copied together, a chunk
+constexpr int CODES = 16 * STEPS * GROUP / 2, CHUNK = CODES + STEPS * 128;  // bytes of its codes; with its scales
 constexpr int MAX_CLUSTER = 8;
 constexpr int PAIR_TOKENS = 2;        // rows of x up to which block scales multiply sums instead of weights
 constexpr int ZEROS = 256;            // bytes of 0 in shared memory, for that
@@ -65,8 +66,8 @@ struct GemvArgs {
 };
 
 __host__ __device__ constexpr int gemv_x_pitch(int kslice) { return kslice * 2 + 64; }  // bytes per row of x
-__host__ __device__ constexpr int gemv_smem(int nt, int depth, int64_t tokens, int kslice, int cluster) {
-  return gemvcfg::WARPS * depth * gemvcfg::SLOT +                                                // ring of weights
+__host__ __device__ constexpr int gemv_smem(int nt, int buffers, int64_t tokens, int kslice, int cluster) {
+  return gemvcfg::WARPS * buffers * gemvcfg::CHUNK +                                             // ring of weights
          2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? gemvcfg::ROUND * 512 * nt : 0) +         // joins
          kslice / gemvcfg::GROUP * 8 * nt * 4 +                                                  // factors of x
          static_cast<int>(tokens < 8 * nt ? tokens : 8 * nt) * gemv_x_pitch(kslice) +            // x
@@ -157,7 +158,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "memory");
   return v;
 }
-// Asynchronous copies to shared memory; bytes past `n` of the 16 or 4 are written as 0.
+// Asynchronous copy to shared memory; bytes past `n` of the 16 are written as 0.
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -166,25 +167,22 @@ __device__ __forceinline__ void copy_async16_hint(uint32_t dst, const void* src,
                "l"(policy)
                : "memory");
 }
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// DEPTH (a power of two): steps of codes and scales in flight per warp.
+// BUFFERS (a power of two): chunks of weights in flight per warp.
 // PAIR: at most two rows of x.
-template <int NT, int DEPTH, bool PAIR>
+template <int NT, int BUFFERS, bool PAIR>
 __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const GemvArgs a) {
   using namespace gemvcfg;
   extern __shared__ __align__(128) uint8_t gemv_smem_raw[];
   const int cluster = 1 << a.cluster_log2, kwarps = 1 << a.kwarps_log2;
   const int pitch = gemv_x_pitch(a.kslice);
-  uint8_t* ring = gemv_smem_raw;                                               // [WARPS][DEPTH][SLOT]
-  float* red = reinterpret_cast<float*>(ring + WARPS * DEPTH * SLOT);          // [2][WARPS][32][4 NT]
+  uint8_t* ring = gemv_smem_raw;                                               // [WARPS][BUFFERS][CHUNK]
+  float* red = reinterpret_cast<float*>(ring + WARPS * BUFFERS * CHUNK);       // [2][WARPS][32][4 NT]
   float* part = red + 2 * WARPS * 128 * NT;                                    // [ROUND][32][4 NT] (clusters)
   float* inv = part + (cluster > 1 ? ROUND * 128 * NT : 0);                    // [groups][8 NT] factors of x
   uint8_t* xs = reinterpret_cast<uint8_t*>(inv + a.kslice / GROUP * 8 * NT);   // [tokens][pitch]
@@ -221,49 +219,55 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
 
   // ---- the walk over weights: step = one 128-column group of one strip ---------------------
   // Every warp takes `per` groups of each of its strips (groups past the slice are skipped), so the
-  // warps of a strip reach its join together. A lane copies its own bytes of the coming DEPTH steps
-  // into its own places of a ring in shared memory, so nothing but its own cp.async groups has to be
-  // waited for. (Loads into registers kept 2 steps in flight in the 128 registers a thread has:
-  // 27.0 us on 2 x 4096 x 24576, bound by the latency of DRAM.)
+  // warps of a strip reach its join together. A warp copies its weights in chunks of STEPS groups: eight
+  // lanes a row, so an instruction covers four rows of the strip (those of one quarter) in whole lines.
+  // The second half of every other row comes first, so that the eight lanes of an access, four of
+  // each of two rows, find different banks.
+  // (Copied by the lane that uses them, 64 bytes a row and 4 bytes of scales at a time, so that nothing else
+  // had to be waited for, they took 35 instructions per step instead of 16. Bulk copies of 256 bytes a
+  // row are limited by the number of copies, 17 cycles each: 98304 rows of 4096 in 57 us.)
   const int wk = warp & (kwarps - 1), wr = warp >> a.kwarps_log2, rows_at_once = WARPS >> a.kwarps_log2;
   const int groups = (klen + GROUP - 1) / GROUP;
   const int gb = wk * a.per;
+  const int my_groups = groups - gb < a.per ? groups - gb : a.per;     // of each strip; may be 0 or less
+  const int chunks = (a.per + STEPS - 1) / STEPS;
+  const int left = klen - gb * GROUP < a.per * GROUP ? klen - gb * GROUP : a.per * GROUP;  // columns of each strip
   const int64_t krow = a.K >> 1;  // bytes of codes per weight row
 
-  // The next step to load. Rows past N and strips past the last load the last ones again: their
-  // results are not stored. Columns past the slice become 0.
+  // The next chunk to load. Rows past N and columns past the slice become 0.
   int l_strip = cid * rows_at_once + wr;
-  int l_step = 0;
-  int l_left;  // columns of the slice from the lane's first one on
-  const uint8_t *l_codes0, *l_codes1, *l_sf;
+  int l_chunk = 0;
+  int l_rows;                    // from the lane's row of quarter 0 to N
+  const uint8_t *l_codes, *l_sf;  // the lane's 16 bytes of quarter 0; of the scales (row lane & 3 of unit lane / 4)
   auto seek = [&]() {
     const int64_t s = l_strip < a.strips ? l_strip : a.strips - 1;
     const int64_t tile = s >> 3;
-    const int r = static_cast<int>(s & 7) * 4 + (g & 3);
-    const int64_t n0 = tile * 128 + (g >> 2) * 32 + r, n1 = n0 + 64;
-    const int k = k0 + gb * GROUP + 32 * t;
-    l_left = klen - gb * GROUP - 32 * t;
-    l_codes0 = a.codes + (n0 < a.N ? n0 : a.N - 1) * krow + (k >> 1);
-    l_codes1 = a.codes + (n1 < a.N ? n1 : a.N - 1) * krow + (k >> 1);
-    l_sf = a.sf + (tile * (a.K >> 6) + (k >> 6)) * 512 + r * 16 + (g >> 2) * 4;
+    const int r = static_cast<int>(s & 7) * 4;
+    const int64_t n = tile * 128 + r + (lane >> 3), k = k0 + gb * GROUP;
+    l_rows = static_cast<int>(a.N - n < 128 ? a.N - n : 128);
+    l_codes = a.codes + n * krow + (k >> 1) + (lane & 7) * 16;
+    l_sf = a.sf + (tile * (a.K >> 6) + (k >> 6) + (lane >> 2)) * 512 + (r + (lane & 3)) * 16;
   };
   // codes are read once per call: they leave L2 first, so that x and what else is used again stay
   const uint64_t once = l2_policy_evict_first();
-  const uint32_t my_ring = smem_u32(ring) + warp * (DEPTH * SLOT);
-  auto load = [&](uint32_t slot) {
+  const uint32_t my_ring = smem_u32(ring) + warp * (BUFFERS * CHUNK);
+  const uint32_t put_at = (lane >> 3) * 128 + (((lane & 7) * 16) ^ ((lane & 8) << 3));
+  auto load = [&](int b) {
     if (l_strip < a.strips) {
-      const int n = l_left > 0 ? 16 : 0;  // past the slice nothing is read
-      const uint32_t c = slot + lane * 16, f = slot + 1024 + lane * 4;
-      copy_async16_hint(c, l_codes0, n, once);
-      copy_async16_hint(c + 512, l_codes1, n, once);
-      copy_async4(f, l_sf, n >> 2);
-      copy_async4(f + 128, l_sf + 8, n >> 2);
-      l_left -= GROUP;
-      l_codes0 += GROUP / 2;
-      l_codes1 += GROUP / 2;
-      l_sf += 1024;
-      if (++l_step == a.per) {
-        l_step = 0;
+      const int cols = left - l_chunk * (STEPS * GROUP);
+      const uint32_t dst = my_ring + b * CHUNK;
+      const int rows = (lane & 7) * 32 < cols ? l_rows : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        copy_async16_hint(dst + q * 512 + put_at, rows > 32 * q ? l_codes + q * 32 * krow : a.codes, rows > 32 * q ? 16 : 0, once);
+      if (lane < 8 * STEPS) {
+        const bool in = (lane >> 2) * 64 < cols;
+        copy_async16(dst + CODES + lane * 16, in ? l_sf : a.sf, in ? 16 : 0);
+      }
+      l_codes += STEPS * (GROUP / 2);
+      l_sf += STEPS * 1024;
+      if (++l_chunk == chunks) {
+        l_chunk = 0;
         l_strip += a.strips_at_once;
         seek();
       }
@@ -271,11 +275,10 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     copy_async_commit();
   };
   seek();
-  // Some steps of weights travel with x, the others follow when x is done: the copies of DEPTH steps
-  // hold a warp up for 5 us, until most of them have arrived.
-  constexpr int FIRST = 4;
+  // Some of the weights travel with x, the others follow when x is done.
+  constexpr int FIRST = BUFFERS;
 #pragma unroll
-  for (int j = 0; j < FIRST; ++j) load(my_ring + j * SLOT);
+  for (int b = 0; b < FIRST; ++b) load(b);
 
   // ---- x to f16, each 128 columns of a row by their power of two -------------------------
   // The largest finite magnitude of a group goes to [2^14, 2^15). A half-warp holds the group, so
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     });
   }
 #pragma unroll
-  for (int j = FIRST; j < DEPTH; ++j) load(my_ring + j * SLOT);
+  for (int b = FIRST; b < BUFFERS; ++b) load(b);
   if constexpr (PAIR) {
     if (tid < ZEROS / 16) reinterpret_cast<uint4*>(xs + tokens * pitch)[tid] = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -336,17 +339,17 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
   const bool holds = (g >> 1) == t;
   const uint8_t* const xpair = holds ? xs + ((g & 1) < tokens ? g & 1 : 0) * pitch + gb * 256 + t * 16 : zeros + t * 16;
   const int xpair_step = holds ? 256 : 0;
-  auto compute_pair = [&](int step, const uint8_t* slot) {
+  auto compute_pair = [&](int step, const uint8_t* codes, const uint8_t* scales) {
     float2 sc[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h2;
-      const uint16_t two = *reinterpret_cast<const uint16_t*>(slot + 1024 + 128 * i + lane * 4 + (t & 1) * 2);
+      const uint16_t two = *reinterpret_cast<const uint16_t*>(scales + 8 * i);
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
       sc[i] = __half22float2(*reinterpret_cast<const __half2*>(&h2));
     }
-    const uint4 q0 = *reinterpret_cast<const uint4*>(slot + lane * 16);
-    const uint4 q1 = *reinterpret_cast<const uint4*>(slot + 512 + lane * 16);
+    const uint4 q0 = *reinterpret_cast<const uint4*>(codes);
+    const uint4 q1 = *reinterpret_cast<const uint4*>(codes + 8 * 128);
     const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w};
     const uint32_t c1[4] = {q1.x, q1.y, q1.z, q1.w};
     const uint8_t* const xp = xpair + step * xpair_step;
@@ -375,18 +378,18 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
       acc[0][i] = fmaf(fmaf(sum[1][i], s.y, sum[0][i] * s.x), i & 1 ? f.y : f.x, acc[0][i]);
     }
   };
-  auto compute = [&](int step, const uint8_t* slot) {
+  auto compute = [&](int step, const uint8_t* codes, const uint8_t* scales) {
     uint32_t s2[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h2;
-      const uint16_t two = *reinterpret_cast<const uint16_t*>(slot + 1024 + 128 * i + lane * 4 + (t & 1) * 2);
+      const uint16_t two = *reinterpret_cast<const uint16_t*>(scales + 8 * i);
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
       s2[i][0] = __byte_perm(h2, h2, 0x1010);
       s2[i][1] = __byte_perm(h2, h2, 0x3232);
     }
-    const uint4 q0 = *reinterpret_cast<const uint4*>(slot + lane * 16);
-    const uint4 q1 = *reinterpret_cast<const uint4*>(slot + 512 + lane * 16);
+    const uint4 q0 = *reinterpret_cast<const uint4*>(codes);
+    const uint4 q1 = *reinterpret_cast<const uint4*>(codes + 8 * 128);
     const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w};
     const uint32_t c1[4] = {q1.x, q1.y, q1.z, q1.w};
     float one[NT][4];
@@ -534,22 +537,34 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     ++it;
   };
 
-  const uint8_t* const ring_warp = ring + warp * (DEPTH * SLOT);
+  // the lane's places in a chunk: its columns of weight row g (row g + 8 is 1024 bytes further), its scales
+  const uint8_t* const my_codes = ring + warp * (BUFFERS * CHUNK) + g * 128 + (g & 1) * 64 + t * 16;
+  const int other = (g & 1) ? -64 : 64;  // to the chunk's second step
+  const uint8_t* const my_scales =
+      ring + warp * (BUFFERS * CHUNK) + CODES + (t >> 1) * 64 + (g & 3) * 16 + (g >> 2) * 4 + (t & 1) * 2;
   int slot = 0;
   while (it < a.iters) {
     const int strip = it * a.strips_at_once + cid * rows_at_once + wr;
     if (cluster == 1 && wk == (it & (kwarps - 1)) && strip < a.strips) load_bias(strip);
-    for (int step = 0; step < a.per; ++step) {
-      copy_async_wait<DEPTH - 1>();
-      if (gb + step < groups) {
-        if constexpr (PAIR) {
-          compute_pair(step, ring_warp + slot * SLOT);
-        } else {
-          compute(step, ring_warp + slot * SLOT);
+    for (int c = 0; c < chunks; ++c) {
+      copy_async_wait<BUFFERS - 1>();
+      __syncwarp();  // other lanes copied what this one reads
+      const uint8_t* const codes = my_codes + slot * CHUNK;
+      const uint8_t* const scales = my_scales + slot * CHUNK;
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        const int step = c * STEPS + j;
+        if (step < my_groups) {
+          if constexpr (PAIR) {
+            compute_pair(step, codes + j * other, scales + j * 128);
+          } else {
+            compute(step, codes + j * other, scales + j * 128);
+          }
         }
       }
-      load(my_ring + slot * SLOT);
-      slot = (slot + 1) & (DEPTH - 1);
+      __syncwarp();  // every lane has read the chunk
+      load(slot);
+      slot = (slot + 1) & (BUFFERS - 1);
     }
     finish();
   }

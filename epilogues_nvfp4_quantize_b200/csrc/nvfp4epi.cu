@@ -877,7 +877,7 @@ bool is_dtype(int d) { return d == NVFP4_OUT_BF16 || d == NVFP4_OUT_F16 || d == 
 template <int NT, bool PAIR>
 nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t stream) {
   using namespace nvfp4::gemvcfg;
-  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 8, PAIR>, nvfp4::gemv_nvfp4_kernel<NT, 4, PAIR>};
+  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 4, PAIR>, nvfp4::gemv_nvfp4_kernel<NT, 2, PAIR>};
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
@@ -919,8 +919,8 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   int depth_i = 0;
   for (int i = 0; i < 4; ++i) {
     const int slice = (groups + (1 << i) - 1) >> i;  // groups per CTA
-    const int d = nvfp4::gemv_smem(NT, 8, a.M, slice * GROUP, 1 << i) <= MAX_SMEM ? 0 : 1;
-    if (d == 1 && nvfp4::gemv_smem(NT, 4, a.M, slice * GROUP, 1 << i) > MAX_SMEM) continue;
+    const int d = nvfp4::gemv_smem(NT, 4, a.M, slice * GROUP, 1 << i) <= MAX_SMEM ? 0 : 1;
+    if (d == 1 && nvfp4::gemv_smem(NT, 2, a.M, slice * GROUP, 1 << i) > MAX_SMEM) continue;
     if (i > 0 && slice * ((1 << i) - 1) >= groups) continue;  // a CTA without columns
     for (int kw = 0; 1 << kw <= WARPS; ++kw) {
       const int per_iter = clusters[i] * (WARPS >> kw);
@@ -948,7 +948,7 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   cfg.numAttrs = a.cluster_log2 > 0 ? 2 : 1;
   cfg.gridDim = dim3(static_cast<unsigned>(n << a.cluster_log2), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)), 1);
   cfg.dynamicSmemBytes =
-      static_cast<size_t>(nvfp4::gemv_smem(NT, depth_i == 0 ? 8 : 4, a.M, a.kslice, 1 << a.cluster_log2));
+      static_cast<size_t>(nvfp4::gemv_smem(NT, depth_i == 0 ? 4 : 2, a.M, a.kslice, 1 << a.cluster_log2));
   if (cudaLaunchKernelEx(&cfg, kerns[depth_i], a) != cudaSuccess) {
     (void)cudaGetLastError();
     return NVFP4_ERR_CUDA;
