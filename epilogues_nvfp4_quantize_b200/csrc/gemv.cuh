@@ -68,7 +68,7 @@ struct GemvArgs {
 __host__ __device__ constexpr int gemv_x_pitch(int kslice) { return kslice * 2 + 64; }  // bytes per row of x
 __host__ __device__ constexpr int gemv_smem(int nt, int buffers, int64_t tokens, int kslice, int cluster) {
   return gemvcfg::WARPS * buffers * gemvcfg::CHUNK +                                             // ring of weights
-         2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? gemvcfg::ROUND * 512 * nt : 0) +         // joins
+         2 * gemvcfg::WARPS * 512 * nt + (cluster > 1 ? 2 * gemvcfg::ROUND * 512 * nt : 0) +     // joins
          kslice / gemvcfg::GROUP * 8 * nt * 4 +                                                  // factors of x
          static_cast<int>(tokens < 8 * nt ? tokens : 8 * nt) * gemv_x_pitch(kslice) +            // x
          (tokens <= gemvcfg::PAIR_TOKENS ? gemvcfg::ZEROS : 0);
@@ -150,14 +150,12 @@ __device__ __forceinline__ void mma_16x8x16_from0(float (&c)[4], uint32_t a0, ui
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Asynchronous copy to shared memory; bytes past `n` of the 16 are written as 0.
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -183,11 +181,12 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
   const int pitch = gemv_x_pitch(a.kslice);
   uint8_t* ring = gemv_smem_raw;                                               // [WARPS][BUFFERS][CHUNK]
   float* red = reinterpret_cast<float*>(ring + WARPS * BUFFERS * CHUNK);       // [2][WARPS][32][4 NT]
-  float* part = red + 2 * WARPS * 128 * NT;                                    // [ROUND][32][4 NT] (clusters)
-  float* inv = part + (cluster > 1 ? ROUND * 128 * NT : 0);                    // [groups][8 NT] factors of x
+  float* part = red + 2 * WARPS * 128 * NT;                                    // [2][ROUND][32][4 NT] (clusters)
+  float* inv = part + (cluster > 1 ? 2 * ROUND * 128 * NT : 0);                // [groups][8 NT] factors of x
   uint8_t* xs = reinterpret_cast<uint8_t*>(inv + a.kslice / GROUP * 8 * NT);   // [tokens][pitch]
 
   griddep_launch_dependents();
+  if (cluster > 1) cluster_arrive();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) & (cluster - 1);
   const int cid = static_cast<int>(blockIdx.x) >> a.cluster_log2;
@@ -275,16 +274,14 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     copy_async_commit();
   };
   seek();
-  // Some of the weights travel with x, the others follow when x is done.
-  constexpr int FIRST = BUFFERS;
 #pragma unroll
-  for (int b = 0; b < FIRST; ++b) load(b);
+  for (int b = 0; b < BUFFERS; ++b) load(b);
 
   // ---- x to f16, each 128 columns of a row by their power of two -------------------------
   // The largest finite magnitude of a group goes to [2^14, 2^15). A half-warp holds the group, so
   // nothing has to be known of the rest of the row, and the products of a group are scaled back when
   // they are added to the others.
-  copy_async_wait<FIRST>();
+  copy_async_wait<BUFFERS>();
   if (a.x_f16 && !a.silu) {  // f16 needs no factor
     for (int i = tid; i < a.kslice / GROUP * 8 * NT; i += THREADS) inv[i] = 1.0f;
   } else {
@@ -312,8 +309,6 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
       *p = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
     });
   }
-#pragma unroll
-  for (int b = FIRST; b < BUFFERS; ++b) load(b);
   if constexpr (PAIR) {
     if (tid < ZEROS / 16) reinterpret_cast<uint4*>(xs + tokens * pitch)[tid] = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -446,7 +441,8 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
     }
   };
 
-  int buf = 0, in_round = 0;
+  if (cluster > 1) cluster_wait();  // every CTA has started: its shared memory can be written to
+  int buf = 0, round_buf = 0, in_round = 0;
   int it = 0, round_base = 0;  // strip iteration, first iteration of the round
   // The end of a strip: its pieces of K are joined over the warps, and over the cluster.
   auto finish = [&]() {
@@ -497,29 +493,33 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i) put(strip, i >> 2, i & 3, sum[i]);
       } else {
-        float* p = part + ((in_round + wr) * 32 + lane) * 4 * NT;
+        // strip s of the round is added up by CTA s modulo `cluster`: its piece goes there
+        const int s = in_round + wr, at = (s & ~(cluster - 1)) + rank;
+        const uint32_t there =
+            mapa_shared(smem_u32(part + ((round_buf * ROUND + at) * 32 + lane) * 4 * NT), s & (cluster - 1));
 #pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) p[i] = sum[i];
+        for (int i = 0; i < NT; ++i)
+          st_cluster_f32x4(there + 16 * i, sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]);
       }
     }
     if (cluster > 1) {
       in_round += rows_at_once;
       if (in_round + rows_at_once > ROUND || it == a.iters - 1) {
-        cluster_sync_all();  // every CTA's pieces of this round's strips are written
+        // Every CTA's pieces of this round's strips are written. The round after the next uses their places
+        // again, behind the next round's barrier, which no CTA reaches before it has read them.
+        cluster_sync_all();
         for (int s = rank + cluster * warp; s < in_round; s += cluster * WARPS) {
           const int st = (round_base + s / rows_at_once) * a.strips_at_once + cid * rows_at_once + s % rows_at_once;
           if (st >= a.strips) continue;
           load_bias(st);
-          const uint32_t at = smem_u32(part + (s * 32 + lane) * 4 * NT);
+          const float* p = part + ((round_buf * ROUND + (s & ~(cluster - 1))) * 32 + lane) * 4 * NT;
           float all[4 * NT];
 #pragma unroll
           for (int i = 0; i < 4 * NT; ++i) all[i] = 0.0f;
-#pragma unroll 4
-          for (int c = 0; c < cluster; ++c) {
-            const uint32_t remote = mapa_shared(at, c);
+          for (int c = 0; c < cluster; ++c, p += 128 * NT) {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              const float4 f = ld_cluster_f32x4(remote + 16 * i);
+              const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
               all[4 * i] += f.x;
               all[4 * i + 1] += f.y;
               all[4 * i + 2] += f.z;
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(gemvcfg::THREADS, 1) gemv_nvfp4_kernel(const G
 #pragma unroll
           for (int i = 0; i < 4 * NT; ++i) put(st, i >> 2, i & 3, all[i]);
         }
-        cluster_sync_all();  // no CTA overwrites or leaves before the others have read
+        round_buf ^= 1;
         in_round = 0;
         round_base = it + 1;
       }
