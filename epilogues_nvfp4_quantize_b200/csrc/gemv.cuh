@@ -7,8 +7,8 @@
 //
 // The product runs on mma.sync.m16n8k16 (f16, float32 accumulators), weights as the 16-row operand
 // and up to 8 rows of x per instruction: with so few rows tcgen05 would need the weights decoded
-// into shared memory first, while here they go from a 16-byte global load through registers into
-// the instruction. A weight's value without G, level x block scale, has at most 6 significant bits
+// into shared memory first, while here they go from shared memory through registers into the
+// instruction. A weight's value without G, level x block scale, has at most 6 significant bits
 // between 2^-10 and 2688 and is exact in f16. x goes to f16 by a power of two for each 128 columns of a
 // row (their largest finite magnitude goes to [2^14, 2^15)): every bf16 value down to 2^-28 of that
 // stays exact and smaller ones are off by at most 2^-39 of it, below float32's own sums; infinities and
@@ -17,10 +17,13 @@
 //
 // A strip is 16 weight rows: rows r .. r+3 of each of the four 32-row quarters of a 128-row scale
 // tile. In the tensor-core scale layout the four quarters' scales of a row are adjacent, so a strip
-// reads whole 32-byte sectors. Lane (g, t) of a warp (g = lane / 4, t = lane % 4) loads 16 bytes of
+// reads whole 32-byte sectors. Lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes 16 bytes of
 // codes at columns 32 t of a 128-column group of its two rows: two whole scale blocks. The order of
 // K within an instruction is free as long as both operands agree, so the lane's bytes feed the
-// instructions in the order they arrive.
+// instructions in the order they come.
+//
+// Measured: 2 x 4096 x 98304 runs at 5.0 TB/s (45 us); of 2 x 4096 x 24576's 16 us, 8.7 are the bytes at the
+// copy rate and about 5 the start (x to every SM and to f16 there, the first weights).
 #pragma once
 
 #include "ptx.cuh"
@@ -33,11 +36,9 @@ namespace gemvcfg {
 constexpr int WARPS = 16;
 constexpr int THREADS = 32 * WARPS;
 constexpr int GROUP = 128;            // columns of K per step of a warp
-constexpr int TILE_TOKENS = 16;       // rows of x per pass over the weight
 constexpr int ROUND = 16;             // strips between two joins of a cluster
 constexpr int STEPS = 2;              // steps whose weights are copied together, a chunk
 constexpr int CODES = 16 * STEPS * GROUP / 2, CHUNK = CODES + STEPS * 128;  // bytes of its codes; with its scales
-constexpr int MAX_CLUSTER = 8;
 constexpr int PAIR_TOKENS = 2;        // rows of x up to which block scales multiply sums instead of weights
 constexpr int ZEROS = 256;            // bytes of 0 in shared memory, for that
 constexpr int MAX_SMEM = 220 * 1024;

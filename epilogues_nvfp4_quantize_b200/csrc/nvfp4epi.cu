@@ -913,9 +913,9 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   // How K is cut: over the CTAs of a cluster and over the warps of a CTA. A larger cluster leaves each CTA
   // less of x to copy and to convert, and a shorter start; what it costs is the joins. In hundredths of a
   // step of all warps (0.4 us): the steps of the longest warp, 100 for each join of warps, 75 for each
-  // CTA in each join of a cluster, 8 for each 128 columns of a row of x. Over 12 shapes of 1 to 16 rows (all
-  // 20 cuts of each measured) the cut so chosen is 2.7 % behind the best on average and 16 % at most; with x
-  // left out and 400 for any join of a cluster it was 18 and 55 %: 1024 x 1024 takes one CTA and 8 warps, the
+  // CTA in each join of a cluster, 8 for each 128 columns of a row of x (12 with SiLU). Over 12 shapes of 1 to
+  // 16 rows (all 20 cuts of each measured) the cut so chosen is 2.2 % behind the best on average and 16 % at
+  // most; with x left out and 400 for any join of a cluster it was 18 and 55 %: 1024 x 1024 takes one CTA and 8 warps, the
   // others mostly 4 CTAs (2 x 4096 x 6144: 6.7 us against 9.0 in one CTA each, 8 x 4096 x 12288: 12.5 against
   // 17.1). Four chunks of weights in flight per warp where they fit beside x, else two.
   const int groups = static_cast<int>((a.K + GROUP - 1) / GROUP);
@@ -932,7 +932,7 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
       const int iters = (a.strips + per_iter - 1) / per_iter;
       const int per = (slice + (1 << kw) - 1) >> kw;
       const int64_t rounds = i == 0 ? 0 : (static_cast<int64_t>(iters) * (WARPS >> kw) + ROUND - 1) / ROUND;
-      const int64_t cost = 100ll * iters * (per + (kw > 0 ? 1 : 0)) + (rounds * 75 << i) + 8 * tokens * slice;
+      const int64_t cost = 100ll * iters * (per + (kw > 0 ? 1 : 0)) + (rounds * 75 << i) + (a.silu ? 12 : 8) * tokens * slice;
       if (best < 0 || cost < best) {
         best = cost;
         buffers_i = d;
