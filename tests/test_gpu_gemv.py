@@ -75,6 +75,20 @@ def test_types_activation_bias(N, K, M, x, out, silu, bias):
     check(torch.from_numpy(xv).to(TYPES[x]).to(device()), nvfp4_from_arrays(*arrays), arrays, out, b, silu)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 20011, 4096), (2, 33000, 2048), (5, 20011, 4096), (13, 20011, 4096), (16, 9000, 8192)])
+def test_many_strips_per_cluster(M, N, K):
+    """Several rounds of joins across the CTAs that share K, the last one not full."""
+    arrays = weight(N, K, N + K)
+    r = np.random.default_rng(M + N)
+    x = torch.from_numpy(r.standard_normal((M, K))).to(torch.bfloat16).to(device())
+    B = nvfp4_from_arrays(*arrays)
+    check(x, B, arrays, "f32", r.standard_normal(N).astype(np.float32))
+    D, E = torch.empty(2, M, N, device=device())
+    for _ in range(3):
+        ep.gemv_nvfp4(x, B, D), ep.gemv_nvfp4(x, B, E)
+        assert torch.equal(D, E), "the same inputs give the same bits"
+
+
 def test_rows_of_very_different_size_and_strides():
     N, K = 256, 1024
     arrays = weight(N, K, 5)
