@@ -1091,6 +1091,8 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 // a column over the warps). With 148 to 2368 slots the kernel is bound by the latency of a thread's loads
 // one after another, and by how many blocks fit at once (32 warps at 64 registers: one per SM, five
 // waves at 4096 columns and 4 sequences).
+// Loads past the end are left out one by one: in a loop unrolled as it is, the remainder's wait for one
+// another (1536 x 2048 with 16 sequences and the weights' sums: 25.9 -> 23.5 us for the whole gradient).
 __global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, 4) norm_grad_reduce_kernel(const NormGradArgs a) {
   using normcfg::REDUCE_WARPS;
   __shared__ float red[3][REDUCE_WARPS][33];
@@ -1110,10 +1112,20 @@ __global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, 4) norm_grad_reduc
     float s0 = 0.0f, s1 = 0.0f;
     if (live && a.w_part != nullptr) {
       const float* p = a.w_part + static_cast<int64_t>(warp) * 2 * a.cols + col;
-#pragma unroll 10
-      for (int g = warp; g < a.chunks; g += REDUCE_WARPS, p += 2 * REDUCE_WARPS * a.cols) {
-        s0 += p[0];
-        s1 += p[a.cols];
+      constexpr int U = 7;
+      for (int g = warp; g < a.chunks; g += U * REDUCE_WARPS) {
+        float u[U][2];
+#pragma unroll
+        for (int i = 0; i < U; ++i, p += 2 * REDUCE_WARPS * a.cols) {
+          const bool in = g + i * REDUCE_WARPS < a.chunks;
+          u[i][0] = in ? p[0] : 0.0f;
+          u[i][1] = in ? p[a.cols] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          s0 += u[i][0];
+          s1 += u[i][1];
+        }
       }
     }
     red[0][warp][lane] = s0;
@@ -1138,11 +1150,21 @@ __global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, 4) norm_grad_reduc
     if (s < e) {
       if (live) {
         const float* p = a.seq_part + (g0 + warp + b) * 3 * a.cols + col;
-#pragma unroll 5
-        for (int g = g0 + warp; g <= g1; g += REDUCE_WARPS, p += 3 * REDUCE_WARPS * a.cols) {
-          v[0] += p[0];
-          v[1] += p[a.cols];
-          v[2] += p[2 * a.cols];
+        constexpr int U = 4;
+        for (int g = g0 + warp; g <= g1; g += U * REDUCE_WARPS) {
+          float u[U][3];
+#pragma unroll
+          for (int i = 0; i < U; ++i, p += 3 * REDUCE_WARPS * a.cols) {
+            const bool in = g + i * REDUCE_WARPS <= g1;
+            u[i][0] = in ? p[0] : 0.0f;
+            u[i][1] = in ? p[a.cols] : 0.0f;
+            u[i][2] = in ? p[2 * a.cols] : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) v[k] += u[i][k];
+          }
         }
       }
     }
