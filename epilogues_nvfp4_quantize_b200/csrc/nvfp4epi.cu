@@ -1313,7 +1313,9 @@ NVFP4_API nvfp4_status residual_norm_backward(const nvfp4_norm_inputs* in, const
   if (st != NVFP4_OK || !(seq || weights)) return st;
   const int64_t by = !seq ? 0 : in->batches < 1024 ? in->batches : 1024;
   const dim3 grid(static_cast<unsigned>((cols + 31) / 32), static_cast<unsigned>(by + 1));
-  return launch_dependent(nvfp4::norm_grad_reduce_kernel, grid, 32 * nvfp4::normcfg::REDUCE_WARPS, 0, stream, a);
+  const bool fits = static_cast<int64_t>(grid.x) * grid.y <= 2ll * info->sm_count;
+  return launch_dependent(fits ? nvfp4::norm_grad_reduce_kernel<2> : nvfp4::norm_grad_reduce_kernel<4>, grid,
+                          32 * nvfp4::normcfg::REDUCE_WARPS, 0, stream, a);
 }
 
 namespace {

@@ -1093,7 +1093,10 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 // waves at 4096 columns and 4 sequences).
 // Loads past the end are left out one by one: in a loop unrolled as it is, the remainder's wait for one
 // another (1536 x 2048 with 16 sequences and the weights' sums: 25.9 -> 23.5 us for the whole gradient).
-__global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, 4) norm_grad_reduce_kernel(const NormGradArgs a) {
+// PER_SM: with 4 blocks per SM a thread has 32 registers, with 2 it has more loads in flight. 2 where all blocks
+// fit at once (1531 x 2048, 3 sequences: 21.6 -> 19.5 us; 16 sequences: 23.5 -> 25.5 us).
+template <int PER_SM>
+__global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, PER_SM) norm_grad_reduce_kernel(const NormGradArgs a) {
   using normcfg::REDUCE_WARPS;
   __shared__ float red[3][REDUCE_WARPS][33];
   griddep_launch_dependents();
@@ -1150,7 +1153,7 @@ __global__ void __launch_bounds__(32 * normcfg::REDUCE_WARPS, 4) norm_grad_reduc
     if (s < e) {
       if (live) {
         const float* p = a.seq_part + (g0 + warp + b) * 3 * a.cols + col;
-        constexpr int U = 4;
+        constexpr int U = PER_SM == 2 ? 7 : 4;
         for (int g = g0 + warp; g <= g1; g += U * REDUCE_WARPS) {
           float u[U][3];
 #pragma unroll
