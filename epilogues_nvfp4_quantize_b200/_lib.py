@@ -574,24 +574,35 @@ def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: 
           None if workspace is None else workspace.data_ptr())
 
 
-def _rows_of_16_bytes(t: torch.Tensor) -> torch.Tensor:
-    """`t`, copied if its rows cannot be read 16 bytes at a time (a broadcast gradient, a view)."""
-    if t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] == 1 or (
-            t.stride(0) >= t.shape[1] and t.stride(0) * t.element_size() % 16 == 0)):
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """`t`, copied unless each of its rows can be read 16 bytes at a time. (A copy by contiguous()
+    would return a contiguous view as it is, wherever it starts.)"""
+    size = t.element_size()
+    if t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+            n == 1 or s * size % 16 == 0 for n, s in zip(t.shape[:-1], t.stride())):
         return t
-    return t.contiguous()
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _rows_of_16_bytes(t: torch.Tensor) -> torch.Tensor:
+    """The same for a matrix whose rows may not overlap either (a broadcast gradient)."""
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        return t.clone(memory_format=torch.contiguous_format)
+    return _aligned(t)
 
 
 class ResidualNorm(torch.autograd.Function):
     """residual_norm with its gradient: apply(x, y, gate, scale, shift, w, w_post, norm, post_norm,
     residual_scale, eps, offsets) returns (x_out, h); h alone without a branch (y None), x_out alone
     with norm None. Rows without a sequence are 0 in the outputs and in the gradients. Parameters'
-    gradients are summed in float32 and returned in the parameter's type."""
+    gradients are summed in float32 and returned in the parameter's type. Inputs and gradients that the
+    kernels cannot read 16 bytes at a time are copied first."""
 
     @staticmethod
     def forward(ctx, x, y=None, gate=None, scale=None, shift=None, w=None, w_post=None, norm="layer",
                 post_norm=False, residual_scale=1.0, eps=1e-6, offsets=None):
         x, y, gate, scale, shift = (None if t is None else _rows_of_16_bytes(t) for t in (x, y, gate, scale, shift))
+        w, w_post = (None if t is None else _aligned(t) for t in (w, w_post))
         make = torch.empty if offsets is None else torch.zeros
         x_out = make(x.shape, dtype=x.dtype, device=x.device) if y is not None else None
         h = make(x.shape, dtype=torch.bfloat16, device=x.device) if norm is not None else None
@@ -688,22 +699,21 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pai
 
 class RopeAxes(torch.autograd.Function):
     """rope_axes with its gradient (the opposite rotation): apply(x, positions, freqs, pairs,
-    interleaved). Positions and frequencies get none."""
+    interleaved). Positions and frequencies get none. x and its gradient are copied first where the
+    kernel cannot read them 16 bytes at a time."""
 
     @staticmethod
     def forward(ctx, x, positions, freqs, pairs, interleaved=True):
         ctx.save_for_backward(positions, freqs)
         ctx.args = (tuple(pairs), interleaved)
-        return rope_axes(x, positions, freqs, pairs, interleaved=interleaved)
+        return rope_axes(_aligned(x), positions, freqs, pairs, interleaved=interleaved)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         positions, freqs = ctx.saved_tensors
         pairs, interleaved = ctx.args
-        if dy.stride(2) != 1 or dy.data_ptr() % 16 or any(s * dy.element_size() % 16 for s in dy.stride()[:2]):
-            dy = dy.contiguous()
-        return rope_axes(dy, positions, freqs, pairs, interleaved=interleaved, inverse=True), None, None, None, None
+        return rope_axes(_aligned(dy), positions, freqs, pairs, interleaved=interleaved, inverse=True), None, None, None, None
 
 
 def read_device_status(stream=None) -> int:

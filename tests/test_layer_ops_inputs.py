@@ -1,0 +1,96 @@
+"""Layouts that the operators between the GEMMs are given in real programs: views that start between 16-byte
+boundaries, single rows of wider buffers. What needs no GPU is tested on the CPU."""
+import pytest
+import torch
+
+import epilogues_nvfp4_quantize_b200 as ep
+from epilogues_nvfp4_quantize_b200 import _lib
+from gpu_util import device
+
+BF = torch.bfloat16
+
+
+def at_offset(t, n):
+    """A contiguous copy of t that starts n elements into its buffer."""
+    buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    out = buf[n:].view(t.shape)
+    out.copy_(t)
+    assert out.is_contiguous() and out.data_ptr() % 16 == n * t.element_size() % 16
+    return out
+
+
+# ---- views that start between 16-byte boundaries ------------------------------------------
+def test_a_contiguous_view_off_a_16_byte_boundary_is_copied():
+    t = at_offset(torch.arange(512, dtype=torch.float32).to(BF).view(8, 64), 1)
+    got = _lib._rows_of_16_bytes(t)
+    assert got.data_ptr() % 16 == 0 and got.is_contiguous() and torch.equal(got, t)
+    one = at_offset(torch.arange(64, dtype=torch.float32).view(1, 64), 1)
+    got = _lib._rows_of_16_bytes(one)
+    assert got.data_ptr() % 16 == 0 and torch.equal(got, one)
+    heads = at_offset(torch.arange(512, dtype=torch.float32).view(4, 2, 64), 3)
+    got = _lib._aligned(heads)
+    assert got.data_ptr() % 16 == 0 and torch.equal(got, heads)
+    w = at_offset(torch.arange(64, dtype=torch.float32), 1)
+    got = _lib._aligned(w)
+    assert got.data_ptr() % 16 == 0 and torch.equal(got, w)
+
+
+def test_what_can_be_read_as_it_is_is_not_copied():
+    t = torch.zeros(8, 80, dtype=BF)
+    for v in (t, t[:, :64], t[:1, 8:72], t[::2]):
+        assert _lib._rows_of_16_bytes(v) is v
+    h = torch.zeros(4, 3, 64, dtype=BF)
+    for v in (h, h[:, :2], h.transpose(0, 1), h[:, :1].expand(4, 3, 64)):
+        assert _lib._aligned(v) is v
+    for v in (t[:, ::2], t[:1].expand(8, 80), t[:, 1:65], torch.zeros(8, 68, dtype=BF)[:, :64]):
+        got = _lib._rows_of_16_bytes(v)
+        assert got is not v and got.is_contiguous() and got.data_ptr() % 16 == 0 and torch.equal(got, v)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stream", [BF, torch.float32])
+def test_residual_norm_gradients_off_a_16_byte_boundary(stream):
+    """The gradient that torch.cat hands back starts wherever its part did."""
+    rows, cols, B = 24, 128, 2
+    g = torch.Generator().manual_seed(1)
+    rn = lambda *s: torch.randn(*s, generator=g).to(device())  # noqa: E731
+    base = dict(x=rn(rows, cols).to(stream), y=rn(rows, cols).to(BF), gate=rn(B, cols), scale=rn(B, cols), shift=rn(B, cols),
+                w=rn(cols), w_post=rn(cols))
+    cx, ch = rn(rows * cols).to(stream), rn(rows * cols).to(BF)
+
+    def run(shifted):
+        leaves = [t.clone().requires_grad_(True) for t in base.values()]
+        # as inputs, views at odd offsets; the gradients come back through cat
+        given = [torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape) for t in leaves] if shifted else leaves
+        x_out, h = ep.ResidualNorm.apply(*given, "layer", True)
+        if shifted:
+            assert any(t.data_ptr() % 16 for t in given)
+            flat = [torch.cat([t.new_zeros(1), t.flatten()])[1:] for t in (x_out, h)]
+        else:
+            flat = [x_out.flatten(), h.flatten()]
+        grads = torch.autograd.grad(flat, leaves, [cx, ch])
+        return [x_out.detach(), h.detach(), *grads]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, torch.float16, torch.float32])
+def test_rope_gradient_off_a_16_byte_boundary(dtype):
+    rows, heads, hd, pairs = 20, 3, 64, [12, 20]
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(rows, heads, hd, generator=g).to(dtype).to(device())
+    c = torch.randn(rows * heads * hd, generator=g).to(dtype).to(device())
+    pos = torch.randint(0, 50, (rows, 2), generator=g).int().to(device())
+    freqs = ep.rope_frequencies(pairs, device=device())
+
+    def run(shifted):
+        leaf = x.clone().requires_grad_(True)
+        given = torch.cat([leaf.new_zeros(1), leaf.flatten()])[1:].view(x.shape) if shifted else leaf
+        r = ep.RopeAxes.apply(given, pos, freqs, pairs)
+        flat = torch.cat([r.new_zeros(1), r.flatten()])[1:] if shifted else r.flatten()
+        return r.detach(), torch.autograd.grad(flat, leaf, c)[0]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
