@@ -403,8 +403,9 @@ def _nvfp4(t: NVFP4Tensor) -> _Tensor:
 
 
 def _pitch(stride, rows: int, cols: int) -> int:
-    """Row pitch from a 2-D tensor's strides. One row has no pitch, and torch may report any."""
-    return stride[0] if rows > 1 else max(stride[0], (cols + 7) // 8 * 8)
+    """Row pitch from a 2-D tensor's strides. One row has no pitch, and torch may report any: it gets
+    that of a buffer of its own."""
+    return stride[0] if rows > 1 else (cols + 7) // 8 * 8
 
 
 def gemv_nvfp4(x: torch.Tensor, B: NVFP4Tensor, D: torch.Tensor, bias: Optional[torch.Tensor] = None,

@@ -94,3 +94,49 @@ def test_rope_gradient_off_a_16_byte_boundary(dtype):
 
     for a, b in zip(run(True), run(False)):
         assert torch.equal(a, b)
+
+
+# ---- single rows of buffers with any pitch --------------------------------------------------
+def one_row(t, pitch):
+    """The values of t (1 x n) as a row of a buffer whose rows are `pitch` elements apart."""
+    return torch.empty_strided(t.shape, (pitch, 1), dtype=t.dtype, device=t.device).copy_(t)
+
+
+def test_one_row_has_no_pitch():
+    for dtype in (BF, torch.float32):
+        t = one_row(torch.zeros(1, 64, dtype=dtype), 101)
+        assert t.stride() == (101, 1)
+        assert _lib._matrix(t, "t", (1, 64), dtype) == (t.data_ptr(), 64)
+        packed, _ = _lib._norm_inputs(t, None, None, t, t, None, None, "layer", False, 1.0, 1e-6, None, None)
+        fields = _lib._NORM_INPUTS.unpack(packed)
+        assert fields[:3] == (1, 64, 1) and [v for v in fields if v == 101] == []
+    two = torch.zeros(2, 72, dtype=BF)[:, :64]
+    assert _lib._matrix(two, "t", (2, 64), BF)[1] == 72
+
+
+@pytest.mark.gpu
+def test_operators_on_one_row_of_an_odd_pitch():
+    K, N, cols = 256, 200, 512
+    g = torch.Generator().manual_seed(3)
+    rn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    W = ep.nvfp4_quantize((rn(N, K) / 16).to(BF).to(device()), ep.NVFP4Tensor.empty(N, K, device()))
+    x = rn(1, K).to(BF).to(device())
+    D, E = torch.zeros(1, N, dtype=BF, device=device()), one_row(torch.zeros(1, N, dtype=BF, device=device()), N + 1)
+    ep.gemv_nvfp4(x, W, D)
+    ep.gemv_nvfp4(one_row(x, K + 5), W, E)
+    assert torch.equal(D, E)
+
+    s = rn(1, cols).to(BF).to(device())
+    y, dxo, dh, gate, scale, shift = (rn(1, cols).to(BF).to(device()) for _ in range(6))
+
+    def run(lay):
+        new = lambda dtype=BF: lay(torch.zeros(1, cols, dtype=dtype, device=device()))  # noqa: E731
+        a = {k: lay(v) for k, v in dict(y=y, gate=gate, scale=scale).items()}
+        xo, h, stats = new(), new(), torch.zeros(1, 4, device=device())
+        ep.residual_norm(lay(s), h, x_out=xo, shift=lay(shift), stats=stats, **a)
+        d = dict(dx=new(), dy=new(), dgate=new(torch.float32), dscale=new(torch.float32), dshift=new(torch.float32))
+        ep.residual_norm_backward(xo, stats, dx_out=lay(dxo), dh=lay(dh), **a, **d)
+        return [xo, h, stats, *d.values()]
+
+    for a, b in zip(run(lambda t: one_row(t, cols + 3)), run(lambda t: t)):
+        assert torch.equal(a, b)
