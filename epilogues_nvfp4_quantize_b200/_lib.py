@@ -139,6 +139,12 @@ def quantize_workspace_bytes() -> int:
     return int(load().nvfp4_quantize_workspace_bytes())
 
 
+def _check_workspace(workspace: torch.Tensor, need: int) -> None:
+    """A workspace has to own the bytes that its size says (an expanded tensor does not)."""
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need} contiguous ones")
+
+
 def _workspace(workspace: Optional[torch.Tensor], compute_amax: bool, device) -> Optional[torch.Tensor]:
     """The caller's workspace (checked for size), or a new one when none is given."""
     if not compute_amax:
@@ -146,8 +152,7 @@ def _workspace(workspace: Optional[torch.Tensor], compute_amax: bool, device) ->
     need = quantize_workspace_bytes()
     if workspace is None:
         return torch.empty((need,), dtype=torch.uint8, device=device)
-    if workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
+    _check_workspace(workspace, need)
     return workspace
 
 
@@ -395,10 +400,14 @@ ACT_SILU = 2
 
 def _nvfp4(t: NVFP4Tensor) -> _Tensor:
     """The C form of an NVFP4 tensor whose buffers are at least as large as its size says (an MXFP4
-    tensor's scales, one per 32 values, are not)."""
+    tensor's scales, one per 32 values, are not) and lie as its layout does."""
     rows, cols = t.rows, t.cols
     if 2 * t.codes.numel() < rows * cols or t.sf.numel() < (rows + 127) // 128 * 128 * ((cols + 63) // 64 * 4):
         raise ValueError(f"codes or scales are too small for an NVFP4 tensor of {rows} x {cols}")
+    if not (t.codes.is_contiguous() and t.sf.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
+    if t.gscale.dtype is not torch.float32:
+        raise ValueError("gscale must be float32")
     return t.c()
 
 
@@ -569,8 +578,8 @@ def residual_norm_backward(x_out: torch.Tensor, stats: torch.Tensor, *, dx_out: 
             # (new_empty takes half of torch.empty's 2 us)
             workspace = x_out.new_empty((need,), dtype=torch.uint8) if stream is None else (
                 _empty_on(stream, (need,), torch.uint8, x_out.device))
-        elif workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
+        else:
+            _check_workspace(workspace, need)
     _call((_lib or load()).residual_norm_backward, "residual_norm_backward", dev, stream, a, stats.data_ptr(), g,
           None if workspace is None else workspace.data_ptr())
 

@@ -140,3 +140,31 @@ def test_operators_on_one_row_of_an_odd_pitch():
 
     for a, b in zip(run(lambda t: one_row(t, cols + 3)), run(lambda t: t)):
         assert torch.equal(a, b)
+
+
+# ---- buffers that hold less memory than they have values --------------------------------------
+def test_buffers_of_repeated_or_scattered_values_are_refused(monkeypatch):
+    u8 = torch.uint8
+    codes, sf, G = torch.zeros(8, 32, dtype=u8), torch.zeros(512, dtype=u8), torch.ones(1)
+    assert _lib._nvfp4(_lib.NVFP4Tensor(codes, sf, G, 8, 64)).rows == 8
+    for bad in ((codes[:1].expand(8, 32), sf, G), (torch.zeros(8, 64, dtype=u8)[:, :32], sf, G),
+                (codes, sf[:1].expand(512), G), (codes, torch.zeros(1024, dtype=u8)[::2], G)):
+        with pytest.raises(ValueError, match="contiguous"):
+            _lib._nvfp4(_lib.NVFP4Tensor(*bad, 8, 64))
+    with pytest.raises(ValueError, match="float32"):
+        _lib._nvfp4(_lib.NVFP4Tensor(codes, sf, G.double(), 8, 64))
+
+    need = ep.residual_norm_workspace_bytes(4, 64, 1)
+    x, stats, dw = torch.zeros(4, 64), torch.zeros(4, 4), torch.zeros(64)
+    monkeypatch.setattr(_lib, "_same_device", lambda *t: 0)
+    monkeypatch.setattr(_lib, "_call", lambda *a: None)
+    call = lambda ws: ep.residual_norm_backward(x, stats, dx_out=x, dh=x.to(BF), dw=dw, workspace=ws)  # noqa: E731
+    call(torch.empty(need, dtype=u8))
+    for bad in (torch.empty(need - 1, dtype=u8), torch.empty(1, dtype=u8).expand(need), torch.empty(2 * need, dtype=u8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            call(bad)
+
+    need = ep.quantize_workspace_bytes()
+    for bad in (torch.empty(1, dtype=u8).expand(need), torch.empty(2 * need, dtype=u8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            _lib._workspace(bad, True, "cpu")
