@@ -386,12 +386,16 @@ def _call(fn, what: str, dev: int, stream, *args) -> None:
         _check(status, what)
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
+
+
 def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
     """An uninitialised tensor that belongs to `stream`: its memory is neither still in use by another
     stream's work nor handed to another one before this stream's work is done."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_object(stream, device)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -421,7 +425,7 @@ def gemv_nvfp4(x: torch.Tensor, B: NVFP4Tensor, D: torch.Tensor, bias: Optional[
                silu: bool = False, stream=None) -> torch.Tensor:
     """D = cast(f(x) (G B)^T + bias) for a few rows x (M x K, bf16 or f16) and an NVFP4 weight B
     (N x K); f is the identity or SiLU; D (M x N) is bf16, f16 or f32 (see gemv_nvfp4 in the
-    header)."""
+    header). For serving: D takes no part in a graph."""
     x_dtype, sx, D_dtype, sD = x.dtype, x.stride(), D.dtype, D.stride()
     if len(sx) != 2 or sx[1] != 1 or (x_dtype is not torch.bfloat16 and x_dtype is not torch.float16):
         raise ValueError("x must be a 2-D bf16 or f16 tensor with unit column stride")
@@ -519,7 +523,7 @@ def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, hq: Optiona
     float32 alike, possibly slices of one tensor. w, w_post: cols float32. offsets: batches + 1
     int32 row offsets on the device (None: sequences of equal length); rows without a sequence are
     left as they are. stats: rows x 4 float32, written for residual_norm_backward. Outputs that are
-    None are not written. Returns (x_out, h, hq)."""
+    None are not written. Returns (x_out, h, hq), which take no part in a graph (ResidualNorm's do)."""
     dev = _same_device(x, h, y, x_out, gate, w_post, w, scale, shift, offsets, stats)
     if hq is not None:
         _same_device(x, hq.codes, hq.sf, hq.gscale)
@@ -682,7 +686,13 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pai
     """Rotary positions on heads x (rows x heads x head_dim; bf16, f16 or f32) into y, which may be
     x itself (None: a new contiguous tensor, allocated on `stream`). positions: rows x axes, int32 or float32; pairs: how
     many pairs each axis turns; freqs: one float64 per pair (rope_frequencies). inverse: the
-    opposite rotation, which is also the gradient (see rope_axes in the header)."""
+    opposite rotation, which is also the gradient (see rope_axes in the header). A new result carries
+    x's gradient, as RopeAxes' does; a given y is written to and takes no part in a graph."""
+    if y is None and x.requires_grad and torch.is_grad_enabled():
+        if stream is None:
+            return RopeAxes.apply(x, positions, freqs, pairs, interleaved, inverse)
+        with torch.cuda.stream(_stream_object(stream, x.device)):
+            return RopeAxes.apply(x, positions, freqs, pairs, interleaved, inverse)
     dtype, sx, shape = x.dtype, x.stride(), x.shape
     if len(sx) != 3 or sx[2] != 1 or dtype not in _OUT_KIND:
         raise ValueError("x must be a rows x heads x head_dim tensor (bf16, f16 or f32) with unit last stride")
@@ -709,21 +719,22 @@ def rope_axes(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, pai
 
 class RopeAxes(torch.autograd.Function):
     """rope_axes with its gradient (the opposite rotation): apply(x, positions, freqs, pairs,
-    interleaved). Positions and frequencies get none. x and its gradient are copied first where the
+    interleaved, inverse). Positions and frequencies get none. x and its gradient are copied first where the
     kernel cannot read them 16 bytes at a time."""
 
     @staticmethod
-    def forward(ctx, x, positions, freqs, pairs, interleaved=True):
+    def forward(ctx, x, positions, freqs, pairs, interleaved=True, inverse=False):
         ctx.save_for_backward(positions, freqs)
-        ctx.args = (tuple(pairs), interleaved)
-        return rope_axes(_aligned(x), positions, freqs, pairs, interleaved=interleaved)
+        ctx.args = (tuple(pairs), interleaved, inverse)
+        return rope_axes(_aligned(x), positions, freqs, pairs, interleaved=interleaved, inverse=inverse)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         positions, freqs = ctx.saved_tensors
-        pairs, interleaved = ctx.args
-        return rope_axes(_aligned(dy), positions, freqs, pairs, interleaved=interleaved, inverse=True), None, None, None, None
+        pairs, interleaved, inverse = ctx.args
+        dx = rope_axes(_aligned(dy), positions, freqs, pairs, interleaved=interleaved, inverse=not inverse)
+        return dx, None, None, None, None, None
 
 
 def read_device_status(stream=None) -> int:

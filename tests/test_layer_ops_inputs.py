@@ -168,3 +168,47 @@ def test_buffers_of_repeated_or_scattered_values_are_refused(monkeypatch):
     for bad in (torch.empty(1, dtype=u8).expand(need), torch.empty(2 * need, dtype=u8)[::2]):
         with pytest.raises(ValueError, match="workspace"):
             _lib._workspace(bad, True, "cpu")
+
+
+# ---- rope_axes' own result in a graph -------------------------------------------------------
+def test_a_new_result_of_rope_axes_carries_its_gradient(monkeypatch):
+    calls = []
+    monkeypatch.setattr(_lib, "_same_device", lambda *t: 0)
+    monkeypatch.setattr(_lib, "_call", lambda *a: calls.append(a))
+    x, pos = torch.zeros(4, 2, 32), torch.zeros(4, 1, dtype=torch.int32)
+    freqs = ep.rope_frequencies([16], device="cpu")
+    assert not ep.rope_axes(x, pos, freqs, [16]).requires_grad
+    x.requires_grad_(True)
+    for inverse in (False, True):
+        r = ep.rope_axes(x, pos, freqs, [16], interleaved=False, inverse=inverse)
+        assert r.requires_grad
+        r.backward(torch.ones_like(r))
+        forward, backward = calls[-2:]
+        assert forward[17:19] == (False, inverse) and backward[17:19] == (False, not inverse)
+    with torch.no_grad():
+        assert not ep.rope_axes(x, pos, freqs, [16]).requires_grad
+    y = torch.zeros(4, 2, 32)
+    assert ep.rope_axes(x, pos, freqs, [16], y) is y and not y.requires_grad  # written to, no graph
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("stream", ["current", "object", "handle"])
+def test_gradient_through_a_new_result_of_rope_axes(inverse, stream):
+    rows, heads, hd, pairs = 33, 2, 64, [12, 16]
+    g = torch.Generator().manual_seed(4)
+    x, c = (torch.randn(rows, heads, hd, generator=g).to(device()) for _ in range(2))
+    pos = torch.randint(0, 90, (rows, 2), generator=g).int().to(device())
+    freqs = ep.rope_frequencies(pairs, device=device())
+    want = ep.rope_axes(x, pos, freqs, pairs, torch.empty_like(x), inverse=inverse)
+    dx = ep.rope_axes(c, pos, freqs, pairs, torch.empty_like(c), inverse=not inverse)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    leaf = x.clone().requires_grad_(True)
+    torch.cuda.synchronize()
+    r = ep.rope_axes(leaf, pos, freqs, pairs, inverse=inverse,
+                     stream=dict(current=None, object=s, handle=s.cuda_stream)[stream])
+    torch.cuda.synchronize()
+    r.backward(c)
+    torch.cuda.synchronize()
+    assert torch.equal(r.detach(), want) and torch.equal(leaf.grad, dx)
