@@ -615,6 +615,8 @@ class ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y=None, gate=None, scale=None, shift=None, w=None, w_post=None, norm="layer",
                 post_norm=False, residual_scale=1.0, eps=1e-6, offsets=None):
+        if y is None and norm is None:
+            raise ValueError("without a branch and a norm there is nothing to compute")
         x, y, gate, scale, shift = (None if t is None else _rows_of_16_bytes(t) for t in (x, y, gate, scale, shift))
         w, w_post = (None if t is None else _aligned(t) for t in (w, w_post))
         make = torch.empty if offsets is None else torch.zeros

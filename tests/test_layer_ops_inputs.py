@@ -212,3 +212,14 @@ def test_gradient_through_a_new_result_of_rope_axes(inverse, stream):
     r.backward(c)
     torch.cuda.synchronize()
     assert torch.equal(r.detach(), want) and torch.equal(leaf.grad, dx)
+
+
+# ---- a call without anything to compute -----------------------------------------------------
+def test_residual_norm_without_a_branch_and_a_norm_is_refused(monkeypatch):
+    monkeypatch.setattr(_lib, "_same_device", lambda *t: 0)
+    monkeypatch.setattr(_lib, "_call", lambda *a: None)
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="branch"):
+        ep.ResidualNorm.apply(x, None, None, None, None, None, None, None)
+    assert ep.ResidualNorm.apply(x, x.to(BF), None, None, None, None, None, None).shape == (4, 64)
+    assert ep.ResidualNorm.apply(x).shape == (4, 64)
