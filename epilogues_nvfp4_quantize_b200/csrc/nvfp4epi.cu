@@ -45,7 +45,7 @@ struct DeviceInfo {
   // clusters of gemv_nvfp4_kernel that fit at once, by log2 of the cluster size (all instances take
   // one CTA per SM)
   int gemv_clusters[4] = {};
-  bool gemv_attr_set[3] = {};
+  bool gemv_attr_set[24] = {};     // gemv_nvfp4_kernel, by NT, PAIR and SILU
   int norm_regs[8] = {};             // registers of residual_norm_ring_kernel, by stream type, NV and POST
   bool norm_grad_attr_set[8] = {};   // residual_norm_grad_kernel, by stream type, POST and CLUSTER
 };
@@ -874,10 +874,12 @@ nvfp4_status launch_dependent(void (*kern)(Args), dim3 grid, int threads, size_t
 
 bool is_dtype(int d) { return d == NVFP4_OUT_BF16 || d == NVFP4_OUT_F16 || d == NVFP4_OUT_F32; }
 
-template <int NT, bool PAIR>
+// a.tile rows of x per CTA: at most 8 NT, 2 with PAIR, half as many with SILU_ROWS.
+template <int NT, int PAIR, int SILU>
 nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t stream) {
   using namespace nvfp4::gemvcfg;
-  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 4, PAIR>, nvfp4::gemv_nvfp4_kernel<NT, 2, PAIR>};
+  void (*const kerns[2])(nvfp4::GemvArgs) = {nvfp4::gemv_nvfp4_kernel<NT, 4, PAIR, SILU>,
+                                             nvfp4::gemv_nvfp4_kernel<NT, 2, PAIR, SILU>};
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
@@ -891,7 +893,7 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   int clusters[4];
   {
     std::lock_guard<std::mutex> lock(g_mutex);
-    bool& set = info->gemv_attr_set[PAIR ? 0 : NT];
+    bool& set = info->gemv_attr_set[NT + 2 * PAIR + 6 * SILU];
     if (!set) {
       for (auto kern : kerns) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM) != cudaSuccess)
@@ -919,20 +921,23 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   // others mostly 4 CTAs (2 x 4096 x 6144: 6.7 us against 9.0 in one CTA each, 8 x 4096 x 12288: 12.5 against
   // 17.1). Four chunks of weights in flight per warp where they fit beside x, else two.
   const int groups = static_cast<int>((a.K + GROUP - 1) / GROUP);
-  const int64_t tokens = a.M < 8 * NT ? a.M : 8 * NT;
+  const int tokens = static_cast<int>(a.M < a.tile ? a.M : a.tile);
+  auto smem = [&](int buffers, int kslice, int cluster) {
+    return nvfp4::gemv_smem(NT, buffers, tokens, SILU ? 2 : 1, kslice, cluster);
+  };
   int64_t best = -1;
   int buffers_i = 0;
   for (int i = 0; i < 4; ++i) {
     const int slice = (groups + (1 << i) - 1) >> i;  // groups per CTA
-    const int d = nvfp4::gemv_smem(NT, 4, a.M, slice * GROUP, 1 << i) <= MAX_SMEM ? 0 : 1;
-    if (d == 1 && nvfp4::gemv_smem(NT, 2, a.M, slice * GROUP, 1 << i) > MAX_SMEM) continue;
+    const int d = smem(4, slice * GROUP, 1 << i) <= MAX_SMEM ? 0 : 1;
+    if (d == 1 && smem(2, slice * GROUP, 1 << i) > MAX_SMEM) continue;
     if (i > 0 && slice * ((1 << i) - 1) >= groups) continue;  // a CTA without columns
     for (int kw = 0; 1 << kw <= WARPS; ++kw) {
       const int per_iter = clusters[i] * (WARPS >> kw);
       const int iters = (a.strips + per_iter - 1) / per_iter;
       const int per = (slice + (1 << kw) - 1) >> kw;
       const int64_t rounds = i == 0 ? 0 : (static_cast<int64_t>(iters) * (WARPS >> kw) + ROUND - 1) / ROUND;
-      const int64_t cost = 100ll * iters * (per + (kw > 0 ? 1 : 0)) + (rounds * 75 << i) + (a.silu ? 12 : 8) * tokens * slice;
+      const int64_t cost = 100ll * iters * (per + (kw > 0 ? 1 : 0)) + (rounds * 75 << i) + (SILU ? 12ll : 8ll) * tokens * slice;
       if (best < 0 || cost < best) {
         best = cost;
         buffers_i = d;
@@ -951,15 +956,41 @@ nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, cudaStream_t strea
   a.strips_at_once = n * per_cluster;
   attr[1].val.clusterDim.x = 1u << a.cluster_log2;
   cfg.numAttrs = a.cluster_log2 > 0 ? 2 : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(n << a.cluster_log2), static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)), 1);
-  cfg.dynamicSmemBytes =
-      static_cast<size_t>(nvfp4::gemv_smem(NT, buffers_i == 0 ? 4 : 2, a.M, a.kslice, 1 << a.cluster_log2));
+  const int64_t tiles = (a.M + a.tile - 1) / a.tile, layers = (tiles + 65534) / 65535;
+  cfg.gridDim = dim3(static_cast<unsigned>(n << a.cluster_log2), static_cast<unsigned>((tiles + layers - 1) / layers),
+                     static_cast<unsigned>(layers));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem(buffers_i == 0 ? 4 : 2, a.kslice, 1 << a.cluster_log2));
   if (cudaLaunchKernelEx(&cfg, kerns[buffers_i], a) != cudaSuccess) {
     (void)cudaGetLastError();
     return NVFP4_ERR_CUDA;
   }
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return NVFP4_OK;
+}
+
+nvfp4_status launch_gemv(DeviceInfo* info, nvfp4::GemvArgs a, bool silu, cudaStream_t stream) {
+  using namespace nvfp4;
+  if (a.M <= gemvcfg::PAIR_TOKENS) {
+    a.tile = static_cast<int>(a.M);
+    return !silu      ? launch_gemv<1, PAIR_LANES, SILU_NO>(info, a, stream)
+           : a.M == 1 ? launch_gemv<1, PAIR_LANES, SILU_ROWS>(info, a, stream)
+                      : launch_gemv<1, PAIR_HALVES, SILU_ROWS>(info, a, stream);
+  }
+  // 16 rows at a time, or 8 (with SiLU then 4) where so many of a very long K do not fit in a cluster's shared memory
+  nvfp4_status st = NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (a.M > 8) {
+    a.tile = 16;
+    st = silu ? launch_gemv<2, PAIR_NO, SILU_PARTS>(info, a, stream) : launch_gemv<2, PAIR_NO, SILU_NO>(info, a, stream);
+  }
+  if (st == NVFP4_ERR_UNSUPPORTED_SHAPE && (!silu || a.M > 4)) {
+    a.tile = 8;
+    st = silu ? launch_gemv<1, PAIR_NO, SILU_PARTS>(info, a, stream) : launch_gemv<1, PAIR_NO, SILU_NO>(info, a, stream);
+  }
+  if (st == NVFP4_ERR_UNSUPPORTED_SHAPE && silu) {
+    a.tile = 4;
+    st = launch_gemv<1, PAIR_NO, SILU_ROWS>(info, a, stream);
+  }
+  return st;
 }
 
 }  // namespace
@@ -988,7 +1019,6 @@ NVFP4_API nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t
   a.M = M;
   a.N = B.rows;
   a.K = B.cols;
-  a.silu = act == NVFP4_ACT_SILU;
   a.codes = static_cast<const uint8_t*>(B.codes);
   a.sf = static_cast<const uint8_t*>(B.sf);
   a.gscale = B.gscale;
@@ -997,10 +1027,7 @@ NVFP4_API nvfp4_status gemv_nvfp4(const void* x, int x_dtype, int64_t M, int64_t
   a.ldd = ldd;
   a.out_kind = out_dtype;
   a.strips = static_cast<int>((B.rows + 127) / 128 * 8);
-  // 16 rows at a time, or 8 where 16 rows of a very long K do not fit in a cluster's shared memory
-  if (M <= nvfp4::gemvcfg::PAIR_TOKENS) return launch_gemv<1, true>(info, a, stream);
-  st = M > 8 ? launch_gemv<2, false>(info, a, stream) : NVFP4_ERR_UNSUPPORTED_SHAPE;
-  return st == NVFP4_ERR_UNSUPPORTED_SHAPE ? launch_gemv<1, false>(info, a, stream) : st;
+  return launch_gemv(info, a, act == NVFP4_ACT_SILU, stream);
 }
 
 namespace {

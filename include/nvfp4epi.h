@@ -298,14 +298,14 @@ nvfp4_status swiglu_bf16(const void* c, int64_t rows, int64_t nh, int64_t ldc,
  * the layout of those GEMMs' B operand; the activations stay in 16 bits.
  *   D[m, n] = cast(G sum_k f(x[m, k]) e2m1(codes[n, k]) e4m3(sf[n, k / 16]) + bias[n])
  *   x: M x K of x_dtype (NVFP4_OUT_BF16 or NVFP4_OUT_F16), leading dimension ldx.
- *   act: NVFP4_ACT_NONE (f the identity) or NVFP4_ACT_SILU (f(x) = x / (1 + exp(-x)), held in f16:
- *        off by at most 2^-11 of itself).
+ *   act: NVFP4_ACT_NONE (f the identity) or NVFP4_ACT_SILU (f(x) = x / (1 + exp(-x)), within 2^-20 of
+ *        itself, or where that is more 2^-38 of the largest finite one of its 128 columns or 2^-119).
  *   bias: N float32, or NULL.  D: M x N of out_dtype, leading dimension ldd elements.
- * Products are exact and sums float32; x is held in f16, scaled by a power of two for each 128 columns
- * of a row, which is exact for every value down to 2^-28 of their largest finite one and off by at most
- * 2^-39 of that below. Infinities and NaN in x reach the outputs of their row only.
- * Rules: 1 <= M <= 524280 (rows are taken 16 at a time: past 16, the weight is read again for each
- *        16 rows), N >= 1, K % 64 == 0, K <= 32768 (UNSUPPORTED_SHAPE); ldx >= K, ldd >= N (INVALID_ARG);
+ * Products are exact and sums, which G multiplies last, float32; x is held in f16 (f(x) of SiLU in two), scaled by
+ * a power of two for each 128 columns of a row, which is exact for every value down to 2^-28 of their largest
+ * finite one and off by at most 2^-39 of that below. Infinities and NaN in x reach the outputs of their row only.
+ * Rules: 1 <= M <= 524280 (rows are taken 16 at a time, or 8 where K is long (or 4 with SiLU): past those, the
+ *        weight is read again), N >= 1, K % 64 == 0, K <= 32768 (UNSUPPORTED_SHAPE); ldx >= K, ldd >= N (INVALID_ARG);
  *        x and ldx*2 bytes, codes and sf 16-byte aligned, bias and gscale 4-byte aligned, D
  *        aligned to its element (MISALIGNED). D may not overlap an input.
  */
