@@ -1168,7 +1168,7 @@ nvfp4_status launch_norm_grad(DeviceInfo* info, nvfp4::NormGradArgs a, cudaStrea
   const int64_t stage = nvfp4::norm_grad_stage(a.cta_cols, sizeof(ST), a.dxo != nullptr, a.dh != nullptr, a.y != nullptr);
   const int64_t vectors = nvfp4::norm_vector_bytes(a.cta_cols, a.mod_f32, (a.gate != nullptr) + (a.scale != nullptr),
                                                    (a.w_post != nullptr) + (a.w != nullptr));
-  int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // the largest size leaves room for three
+  int64_t stages = (SMEM / per_sm - SMEM_OTHER - vectors) / stage;  // two at least, whatever width and types
   const int64_t most = (a.rows + a.chunks - 1) / a.chunks;
   if (stages > GRAD_MAX_STAGES) stages = GRAD_MAX_STAGES;
   if (stages > most) stages = most;

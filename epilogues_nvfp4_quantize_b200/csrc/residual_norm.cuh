@@ -349,8 +349,20 @@ constexpr int FWD_MAX_STAGES = 8;
 // 4096 columns 10.7 / 13.6, 8192 10.8 / 13.4, 1024 11.8 / 15.5.
 constexpr int RING_ROWS = 3;
 constexpr int SMEM = 220 * 1024;         // per SM, for its CTAs' row buffers and SMEM_OTHER each
-constexpr int SMEM_OTHER = 3584;         // a CTA's static and reserved shared memory
+constexpr int SMEM_OTHER = 3584;         // a CTA's static and reserved (1 KB) shared memory
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
+constexpr int GRAD_MAX_STAGES = 8;
+constexpr int REDUCE_WARPS = 16;
+// Static shared memory: the sums (`floats`), the barriers and a flag.
+constexpr int smem_static(int floats, int barriers) { return 4 * floats + 8 * barriers + 8; }
+constexpr int FWD_RED = 2 * 3 * 16;      // floats for the sums of the ring kernel
+__host__ __device__ constexpr int grad_red(bool cluster) { return (cluster ? 4 : 1) * 16 * 8; }  // half the gradient's
+static_assert(1024 + smem_static(FWD_RED, FWD_MAX_STAGES + 1) <= SMEM_OTHER, "ring kernel");
+static_assert(1024 + smem_static(2 * grad_red(false), GRAD_MAX_STAGES + 1) <= SMEM_OTHER, "gradient");
+// Where a cluster shares a row, its sums need more than SMEM_OTHER; a CTA then has its SM to itself (from 4104 columns
+// on it has more than GRAD_THREADS / 2 threads), and they lie in what SMEM leaves of the SM's 228 KB and the CTA's 227.
+static_assert(SMEM - SMEM_OTHER + 1024 + smem_static(2 * grad_red(true), GRAD_MAX_STAGES + 1) <= 228 * 1024, "");
 }  // namespace normcfg
 
 // A sequence's vectors on their way to a CTA's registers: one bulk copy each into shared memory, all in
@@ -407,7 +419,8 @@ template <class ST, int NV, bool POST>
 __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormArgs a) {
   using namespace normcfg;
   extern __shared__ __align__(128) uint8_t norm_rows[];
-  __shared__ float red[2][3][16];
+  __shared__ float red[2][3][16];  // FWD_RED
+  static_assert(sizeof(red) == 4 * FWD_RED, "");
   __shared__ __align__(8) uint64_t full[FWD_MAX_STAGES], vec_full;
   __shared__ int abort_flag;
   griddep_launch_dependents();
@@ -742,12 +755,6 @@ struct NormGradArgs {
   int* seq_pieces;        // batches x 2: the first and the last piece that hold rows of a sequence
 };
 
-namespace normcfg {
-constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
-constexpr int GRAD_MAX_STAGES = 8;
-constexpr int REDUCE_WARPS = 16;
-}  // namespace normcfg
-
 // Bytes of one row's buffer: the stream, its gradient, the gradient of h, the branch, the statistics
 // (absent ones take no room).
 __host__ __device__ constexpr int64_t norm_grad_stage(int64_t cols, int elem, bool dxo, bool dh, bool y) {
@@ -822,7 +829,7 @@ template <class ST, bool POST, bool CLUSTER>
 __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_kernel(const NormGradArgs a) {
   using namespace normcfg;
   extern __shared__ __align__(128) uint8_t norm_rows[];
-  __shared__ float red[2][(CLUSTER ? 4 : 1) * 16 * 8];
+  __shared__ float red[2][grad_red(CLUSTER)];
   __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES], vec_full;
   __shared__ int abort_flag;
   griddep_launch_dependents();
@@ -1088,9 +1095,9 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 // Adds up the slots of each sequence and the pieces' weight sums. Block (x, y): columns 32 x and
 // on; y < gridDim.y - 1 takes the sequences y, y + gridDim.y - 1, ..., the last y the weights.
 // 16 warps share the slots, one column per lane, and are joined in a fixed order (a half-warp then adds
-// a column over the warps). With 148 to 2368 slots the kernel is bound by the latency of a thread's loads
-// one after another, and by how many blocks fit at once (32 warps at 64 registers: one per SM, five
-// waves at 4096 columns and 4 sequences).
+// a column over the warps). With 148 to 2368 pieces (74 or 32 where a cluster shares a row;
+// never more than rows) the kernel is bound by the latency of a thread's loads one after another, and by how
+// many blocks fit at once (32 warps at 64 registers: one per SM, five waves at 4096 columns and 4 sequences).
 // Loads past the end are left out one by one: in a loop unrolled as it is, the remainder's wait for one
 // another (1536 x 2048 with 16 sequences and the weights' sums: 25.9 -> 23.5 us for the whole gradient).
 // PER_SM: with 4 blocks per SM a thread has 32 registers, with 2 it has more loads in flight. 2 where all blocks
