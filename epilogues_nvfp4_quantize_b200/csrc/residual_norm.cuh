@@ -354,8 +354,8 @@ constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int GRAD_THREADS = 512;        // threads per SM that the gradient kernel's registers allow
 constexpr int GRAD_MAX_STAGES = 8;
 constexpr int REDUCE_WARPS = 16;
-// Static shared memory: the sums (`floats`), the barriers and a flag.
-constexpr int smem_static(int floats, int barriers) { return 4 * floats + 8 * barriers + 8; }
+// Static shared memory: the sums (`floats`), the barriers and what a wait that gave up leaves.
+constexpr int smem_static(int floats, int barriers) { return 4 * floats + 8 * barriers + 16; }
 constexpr int FWD_RED = 2 * 3 * 16;      // floats for the sums of the ring kernel
 __host__ __device__ constexpr int grad_red(bool cluster) { return (cluster ? 4 : 1) * 16 * 8; }  // half the gradient's
 static_assert(1024 + smem_static(FWD_RED, FWD_MAX_STAGES + 1) <= SMEM_OTHER, "ring kernel");
@@ -406,6 +406,17 @@ __device__ __forceinline__ int64_t norm_chunk_row(int64_t each, int extra, int g
   return each * g + (g < extra ? g : extra);
 }
 
+// Warp 0, after its last row, where its wait for row `row` of `rows` gave up (from then on it fetched nothing more):
+// the copies that were in flight, of `row` and the rows behind it that the ring holds and of a sequence's vectors,
+// are waited for once more, so that none arrives in shared memory that is no longer this CTA's.
+__device__ __noinline__ void norm_drain(uint64_t* full, uint64_t* vec_full, uint32_t vec_phase, int row, int64_t rows,
+                                        int stages) {
+  constexpr uint64_t LIMIT_NS = normcfg::WAIT_LIMIT_NS / 8;
+  (void)mbar_wait(vec_full, vec_phase, nullptr, LIMIT_NS, 84);
+  for (int r = row; r < row + stages && r < rows; ++r)
+    (void)mbar_wait(&full[r % stages], static_cast<uint32_t>(r / stages) & 1u, nullptr, LIMIT_NS, 84);
+}
+
 // residual_norm over many rows: a CTA walks a contiguous piece of them. Rows come through a ring of
 // row buffers, filled by bulk copies (one per tensor and row, issued by one warp `stages` rows
 // ahead), so coming rows are in flight while a row is reduced. A row's first barrier also frees its
@@ -422,7 +433,8 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
   __shared__ float red[2][3][16];  // FWD_RED
   static_assert(sizeof(red) == 4 * FWD_RED, "");
   __shared__ __align__(8) uint64_t full[FWD_MAX_STAGES], vec_full;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, stuck_row;
+  __shared__ uint32_t stuck_vectors;
   griddep_launch_dependents();
   const int g = blockIdx.x;
   const int64_t r0 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g), r1 = norm_chunk_row(a.chunk_rows, a.chunk_extra, g + 1);
@@ -555,7 +567,17 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
 
   int stage = 0;
   uint32_t phase = 0u, vec_phase = 0u;
+  bool arrives = true;  // no wait of warp 0 has given up
+  auto fetch_next = [&](int64_t row, bool in_time) {  // warp 0, once the buffer of `row` is free
+    if (!__all_sync(0xffffffffu, in_time || !arrives)) {
+      arrives = false;
+      stuck_row = static_cast<int>(row - r0);
+      stuck_vectors = vec_phase ^ 1u;  // of the vectors that were waited for last
+    }
+    if (arrives && row + a.stages < r1) fetch(row + a.stages, stage);
+  };
   for (int64_t row = r0; row < r1; ++row) {
+    bool in_time = true;
     if (row >= seq_end) {
       if (row != r0) b = norm_sequence(a.offsets, a.batches, a.rows_per_batch, row);
       if (b < 0) {  // rows without a sequence are left as they are
@@ -564,8 +586,8 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
         seq_end = a.offsets == nullptr ? (b + 1) * a.rows_per_batch : static_cast<int64_t>(a.offsets[b + 1]);
         if constexpr (NC == NV) {
           // a barrier lies behind since the last sequence's were read
-          if (threadIdx.x == 0 && row != r0) fetch_vectors();
-          (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 82);
+          if (threadIdx.x == 0 && row != r0 && arrives) fetch_vectors();
+          in_time = mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 82);
           vec_phase ^= 1u;
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
@@ -574,11 +596,11 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
         }
       }
     }
-    (void)mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 81);
+    in_time = mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 81) && in_time;
     const uint8_t* buf = norm_rows + stage * stage_bytes;
     bool freed = false;  // a barrier has been passed since the row's values were read
     auto refill = [&]() {
-      if (!freed && threadIdx.x < 32 && row + a.stages < r1) fetch(row + a.stages, stage);
+      if (!freed && threadIdx.x < 32) fetch_next(row, in_time);
       freed = true;
     };
     if (b >= 0) {
@@ -696,6 +718,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const NormAr
       phase ^= 1u;
     }
   }
+  if (!arrives) norm_drain(full, &vec_full, stuck_vectors, stuck_row, r1 - r0, a.stages);
 }
 
 // =====================================================================================
@@ -831,7 +854,8 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
   extern __shared__ __align__(128) uint8_t norm_rows[];
   __shared__ float red[2][grad_red(CLUSTER)];
   __shared__ __align__(8) uint64_t full[GRAD_MAX_STAGES], vec_full;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, stuck_row;
+  __shared__ uint32_t stuck_vectors;
   griddep_launch_dependents();
   constexpr int NV = 1;
   const int cluster = CLUSTER ? a.cluster : 1;
@@ -951,8 +975,17 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
 
   int stage = 0;
   uint32_t phase = 0u, vec_phase = 0u;
+  bool arrives = true;  // no wait of warp 0 has given up
+  auto fetch_next = [&](int64_t row, bool in_time) {  // warp 0, once the buffer of `row` is free
+    if (!__all_sync(0xffffffffu, in_time || !arrives)) {
+      arrives = false;
+      stuck_row = static_cast<int>(row - r0);
+      stuck_vectors = vec_phase ^ 1u;  // of the vectors that were waited for last
+    }
+    if (arrives && row + a.stages < r1) fetch(row + a.stages, stage);
+  };
   for (int64_t row = r0; row < r1; ++row) {
-    bool skip = false;
+    bool skip = false, in_time = true;
     if (row >= seq_end) {
       if (row != r0) {
         if (b >= 0) flush(row);
@@ -971,8 +1004,8 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
         }
         {
           // a barrier lies behind since the last sequence's were read
-          if (threadIdx.x == 0 && row != r0) fetch_vectors();
-          (void)mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 83);
+          if (threadIdx.x == 0 && row != r0 && arrives) fetch_vectors();
+          in_time = mbar_wait(&vec_full, vec_phase, &abort_flag, WAIT_LIMIT_NS, 83);
           vec_phase ^= 1u;
           if (live[0]) {
             float v[8];
@@ -988,7 +1021,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
         }
       }
     }
-    (void)mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 80);
+    in_time = mbar_wait(&full[stage], phase, &abort_flag, WAIT_LIMIT_NS, 80) && in_time;
     const uint8_t* buf = norm_rows + stage * stage_bytes;
     if (skip) {
       if constexpr (CLUSTER) {
@@ -1044,6 +1077,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
         }
       }
       row_sums<POST ? 6 : 2, CLUSTER>(s, red[static_cast<int>(row - r0) & 1], rank, cluster);
+      if (!CLUSTER && threadIdx.x < 32) fetch_next(row, in_time);
       const float m1 = a.norm == NORM_LAYER ? s[0] * inv_n : 0.0f, m2 = s[1] * inv_n;
       const float m3 = POST ? (s[2] + rstd * (s[3] - m1 * s[4] - m2 * s[5])) * inv_n : 0.0f;
 #pragma unroll
@@ -1071,8 +1105,9 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
         }
       }
     }
-    // every thread has passed this row's barrier, so its buffer takes the next row
-    if (threadIdx.x < 32 && row + a.stages < r1) fetch(row + a.stages, stage);
+    // Every thread has passed this row's barrier, so its buffer takes the next row. (A CTA with whole rows asks for it
+    // right behind the barrier, a cluster's here: 16384 x 4096 153 and 157 us, 8192 x 5120 203 and 193 us.)
+    if ((CLUSTER || skip) && threadIdx.x < 32) fetch_next(row, in_time);
     if (++stage == a.stages) {
       stage = 0;
       phase ^= 1u;
@@ -1089,6 +1124,7 @@ __global__ void __launch_bounds__(normcfg::GRAD_THREADS, 1) residual_norm_grad_k
       }
     }
   }
+  if (!arrives) norm_drain(full, &vec_full, stuck_vectors, stuck_row, r1 - r0, a.stages);
   if constexpr (CLUSTER) cluster_sync_all();  // no CTA leaves while another may write its sums there
 }
 
