@@ -109,6 +109,12 @@ def test_several_passes_with_several_rounds_of_joins(M, N, K, silu, out):
     check_against_the_form(M, N, K, silu, out)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("N,K,out", [(20011, 4096, "f32"), (9001, 6208, "f16")])
+def test_silu_of_few_rows_with_several_rounds_of_joins(M, N, K, out):
+    check_against_the_form(M, N, K, True, out)
+
+
 @pytest.mark.parametrize("M,K", [(2, 32768), (7, 32768), (8, 32768), (9, 10240), (16, 10304), (12, 16384), (20, 30016)])
 def test_silu_of_long_rows(M, K):
     """Where two f16 for each of 16 or 8 rows do not fit in a cluster, fewer rows are taken at a time."""
